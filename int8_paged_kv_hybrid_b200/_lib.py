@@ -1,4 +1,4 @@
-"""ctypes binding of libhybkv.so (the C ABI in include/hyb_kv.h).
+"""ctypes binding of libhybkv.so (the C ABI in include/hyb_kv.h and include/hyb_spec.h).
 
 Argument marshalling only: every step of the decode path runs in the CUDA
 library.  Tensors are PyTorch CUDA tensors (PyTorch provides device memory
@@ -27,6 +27,11 @@ HYB_STATUS_CAPACITY = 3
 HYB_STATUS_SEQ_LEN = 4
 HYB_STATUS_TIMEOUT = 5
 HYB_STATUS_BAD_TIER = 6
+HYB_STATUS_POOL = 7
+HYB_STATUS_BAD_TREE = 8
+
+HYB_MAX_TREE = 64
+HYB_SLOT_NONE = -1
 
 EXPORTED = (
     "hyb_check_desc", "hyb_kv_append", "hyb_decode_plan", "hyb_decode_workspace_bytes",
@@ -36,6 +41,8 @@ EXPORTED = (
     "hyb_kv_migrate", "hyb_migration_threshold_ms", "hyb_migration_decision",
     "hyb_decode_attn_sparse", "hyb_decode_sparse_workspace_bytes", "hyb_decode_sparse_selection",
     "hyb_sparse_top_k", "hyb_set_wait_limit", "hyb_decode_launch_info", "hyb_stream_read",
+    "hyb_tree_attn", "hyb_tree_workspace_bytes", "hyb_check_pool", "hyb_pool_resize",
+    "hyb_pool_workspace_bytes", "hyb_slot_map",
 )
 
 
@@ -64,6 +71,23 @@ class CacheDesc(ctypes.Structure):
         ("block_table", ctypes.c_void_p),
         ("seq_lens", ctypes.c_void_p),
         ("n_int4_blocks", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class PoolDesc(ctypes.Structure):
+    """Mirror of hyb_pool_desc."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("num_phys_blocks", ctypes.c_int32),
+        ("hot_tokens", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("ring", ctypes.c_void_p),
+        ("state", ctypes.c_void_p),
+        ("n_blocks", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
     ]
 
@@ -115,10 +139,20 @@ def load(path: str = LIB_PATH):
     lib.hyb_read_status.argtypes = [D, ctypes.POINTER(i32), i32, P]
     lib.hyb_stream_read.argtypes = [P, sz, P, P]
     lib.hyb_stream_read.restype = ctypes.c_int
+    B = ctypes.POINTER(PoolDesc)
+    lib.hyb_tree_attn.argtypes = [D, P, P, P, P, P, i32, ctypes.c_float, P, sz, P, P, P]
+    lib.hyb_tree_workspace_bytes.argtypes = [D, i32]
+    lib.hyb_tree_workspace_bytes.restype = sz
+    lib.hyb_check_pool.argtypes = [B]
+    lib.hyb_pool_resize.argtypes = [B, B, P, P, sz, P]
+    lib.hyb_pool_workspace_bytes.argtypes = [B]
+    lib.hyb_pool_workspace_bytes.restype = sz
+    lib.hyb_slot_map.argtypes = [B, P, P, P, i32, P, P, P]
     lib.hyb_strerror.argtypes = [ctypes.c_int]
     lib.hyb_strerror.restype = ctypes.c_char_p
     for name in ("hyb_check_desc", "hyb_kv_append", "hyb_decode_plan", "hyb_decode_attn", "hyb_decode_step",
-                 "hyb_combine", "hyb_read_status", "hyb_last_cuda_error", "hyb_version", "hyb_kv_migrate"):
+                 "hyb_combine", "hyb_read_status", "hyb_last_cuda_error", "hyb_version", "hyb_kv_migrate",
+                 "hyb_tree_attn", "hyb_check_pool", "hyb_pool_resize", "hyb_slot_map"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -288,3 +322,54 @@ def hyb_stream_read(src, sink, stream=None) -> None:
 
 def hyb_version() -> int:
     return load().hyb_version()
+
+
+# ---- speculative decoding (include/hyb_spec.h) ----
+
+def hyb_tree_workspace_bytes(desc, max_tree) -> int:
+    return int(load().hyb_tree_workspace_bytes(ctypes.byref(desc), int(max_tree)))
+
+
+def hyb_tree_attn(desc, q, k_tree, v_tree, tree_mask, n_tree, max_tree, softmax_scale, workspace, out,
+                  lse_out=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().hyb_tree_attn(ctypes.byref(desc), _ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(tree_mask),
+                                _ptr(n_tree), int(max_tree), float(softmax_scale), _ptr(workspace), ws_bytes,
+                                _ptr(out), _ptr(lse_out), _stream(stream)), "hyb_tree_attn")
+
+
+def hyb_check_pool(pool: PoolDesc) -> int:
+    return load().hyb_check_pool(ctypes.byref(pool))
+
+
+def hyb_pool_workspace_bytes(pool) -> int:
+    return int(load().hyb_pool_workspace_bytes(ctypes.byref(pool)))
+
+
+def hyb_pool_resize(pool, to, lens, workspace, stream=None):
+    """to: a PoolDesc, or None for in place."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().hyb_pool_resize(ctypes.byref(pool), None if to is None else ctypes.byref(to), _ptr(lens),
+                                  _ptr(workspace), ws_bytes, _stream(stream)), "hyb_pool_resize")
+
+
+def hyb_slot_map(pool, lens, first, n_tok, max_total, cu, slots, stream=None):
+    _check(load().hyb_slot_map(ctypes.byref(pool), _ptr(lens), _ptr(first), _ptr(n_tok), int(max_total), _ptr(cu),
+                               _ptr(slots), _stream(stream)), "hyb_slot_map")
+
+
+def need(ok, what):
+    """Raise HYB_ERR_INVALID_VALUE unless ok."""
+    if not ok:
+        raise HybError(HYB_ERR_INVALID_VALUE, what)
+
+
+def on_device(device, stream, call):
+    """call(stream) on `stream`, by default the current stream of `device`
+    (which need not be the current device)."""
+    import torch
+    need(device.type == "cuda", "a call on %s buffers" % device)
+    if device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream() if stream is None else stream)
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream(device) if stream is None else stream)

@@ -14,6 +14,15 @@ HOT, BLOCK, HEAD_DIM = 32, 64, 128
 TILE_BYTES = BLOCK * HEAD_DIM
 
 
+def indexed_device(device):
+    """torch.device with its index (the current device's where none is given)."""
+    import torch
+    dev = torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return dev
+
+
 class HybridKVCache:
     def __init__(self, batch, num_kv_heads, num_q_heads, num_phys_blocks, max_blocks_per_seq,
                  quant_bits=8, block_table=None, n_int4=None, device="cuda", hot_tokens=HOT,
@@ -24,7 +33,7 @@ class HybridKVCache:
         self.quant_bits = int(quant_bits)
         self.hot_tokens = int(hot_tokens)
         self.block_size = int(block_size)
-        dev = torch.device(device)
+        dev = indexed_device(device)
         self.device = dev
         self.hot = torch.zeros((self.batch, self.hkv, self.hot_tokens, 2, HEAD_DIM), dtype=torch.float16,
                                device=dev)
@@ -153,6 +162,43 @@ class HybridKVCache:
             workspace = self.step_workspace(max_seq_len, split_tokens)
         _lib.hyb_decode_step(self.desc, n_new, k_new, v_new, q, softmax_scale, max_seq_len, split_tokens,
                              workspace, out, lse, stream)
+        return out
+
+    def tree_workspace(self, max_tree):
+        """Workspace of tree_decode for trees of up to max_tree nodes (any lengths)."""
+        import torch
+        n = _lib.hyb_tree_workspace_bytes(self.desc, max_tree)
+        _lib.need(n > 0, "tree_workspace: max_tree %r" % (max_tree,))
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def tree_decode(self, q, k_tree, v_tree, tree_mask, softmax_scale, n_tree=None, out=None, lse=None,
+                    workspace=None, stream=None):
+        """Attention of drafted nodes (hyb_tree_attn): q FP16 CUDA
+        [batch][nodes][Hq][128], k_tree / v_tree FP16 [batch][nodes][Hkv][128],
+        tree_mask int64 [batch][nodes] (bit j: the node attends node j; see
+        tree_masks) or None for a chain, n_tree int32 [batch] or None for all
+        nodes -> out FP16 [batch][nodes][Hq][128] (and lse FP32
+        [batch][nodes][Hq]).  Rows at and behind n_tree[b] are left as they
+        were (zero, and -inf, in an `out` and a `lse` that this call makes)."""
+        import torch
+        need, dev, nodes = _lib.need, self.device, q.shape[1] if q.dim() == 4 else 0
+        kv_shape = (self.batch, nodes, self.hkv, HEAD_DIM)
+        if out is None:
+            out = torch.zeros((self.batch, nodes, self.hq, HEAD_DIM), dtype=torch.float16, device=dev)
+        for name, x, shape in (("q", q, (self.batch, nodes, self.hq, HEAD_DIM)), ("k_tree", k_tree, kv_shape),
+                               ("v_tree", v_tree, kv_shape), ("out", out, (self.batch, nodes, self.hq, HEAD_DIM))):
+            need(x.shape == shape and x.dtype == torch.float16 and x.device == dev and x.is_contiguous(),
+                 "tree_decode: " + name)
+        for name, x, shape, dtype in (("tree_mask", tree_mask, (self.batch, nodes), torch.int64),
+                                      ("n_tree", n_tree, (self.batch,), torch.int32),
+                                      ("lse", lse, (self.batch, nodes, self.hq), torch.float32)):
+            need(x is None or (x.shape == shape and x.dtype == dtype and x.device == dev and x.is_contiguous()),
+                 "tree_decode: " + name)
+        if workspace is None:
+            workspace = self.tree_workspace(nodes)
+        need(workspace.device == dev and workspace.is_contiguous(), "tree_decode: workspace")
+        _lib.on_device(dev, stream, lambda s: _lib.hyb_tree_attn(
+            self.desc, q, k_tree, v_tree, tree_mask, n_tree, nodes, softmax_scale, workspace, out, lse, s))
         return out
 
     def status(self, clear=False, stream=None):

@@ -11,6 +11,7 @@
 
 #include "hyb_measure.h"
 #include "kernels.cuh"
+#include "spec.cuh"
 
 namespace {
 
@@ -50,6 +51,17 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
 
+namespace hyb {
+
+int host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+int host_sm_count() { return sm_count(); }
+long long host_wait_cycles() {
+  const long long w = g_wait_cycles.load(std::memory_order_relaxed);
+  return w > 0 ? w : kDefaultWaitCycles;
+}
+
+}  // namespace hyb
+
 extern "C" {
 
 int hyb_version(void) { return 10000; }
@@ -88,6 +100,8 @@ const char *hyb_strerror(int code) {
     case 100 + HYB_STATUS_TIMEOUT: return "device status: a bounded wait in a kernel ran out";
     case 100 + HYB_STATUS_BAD_TIER:
       return "device status: a migration target outside the block table or beyond max_delta";
+    case 100 + HYB_STATUS_POOL: return "device status: too few free blocks in the pool, or contradictory pool counts";
+    case 100 + HYB_STATUS_BAD_TREE: return "device status: n_tree out of range";
     default: return "unknown code";
   }
 }
@@ -450,8 +464,7 @@ static int decode_launch(const hyb_cache_desc *d, const void *q, float softmax_s
   a.v_new = static_cast<const __half *>(v_new);
   a.seq_cnt = step ? reinterpret_cast<int32_t *>(ws + wl.seq_cnt) : nullptr;
   a.l2_skip = l2_skip ? 1 : 0;
-  const long long wait = g_wait_cycles.load(std::memory_order_relaxed);
-  a.wait_cycles = wait > 0 ? wait : hyb::kDefaultWaitCycles;
+  a.wait_cycles = hyb::host_wait_cycles();
   a.batch = d->batch;
   const bool persist = pl.persist && !l2_skip;
   a.unit_ctr = pl.persist ? reinterpret_cast<int32_t *>(ws + wl.unit_ctr) : nullptr;

@@ -29,6 +29,14 @@ struct TreeArgs {
   int lsub;                   // log2 of the 64-token sub-blocks per block
   int bshift;                 // log2 of the tokens per block
   float qk_scale;             // softmax_scale * log2(e)
+  long long wait_cycles;      // limit (SM cycles) of the bounded waits
+  int ctas;                   // CTAs of the launch
+  // partial results of units that several CTAs share (see tree.cu): sums and
+  // maxima [2 ctas][rows], outputs [2 ctas][32][rows][4], rows = 128 * MT, and
+  // the CTAs {first, last} of every unit [batch][Hkv][groups]
+  float *part_ml;
+  float *part_o;
+  int2 *unit_ctas;
 };
 
 struct PoolArgs {
@@ -54,6 +62,13 @@ struct SlotArgs {
 };
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream);
+// 128-row tiles a CTA takes at once for trees of max_tree nodes, and the row
+// groups of that many tiles a (sequence, kv head) can have
+inline int tree_m_tiles(int max_tree, int group) { return max_tree * group > 128 ? 2 : 1; }
+inline int tree_groups(int max_tree, int group) {
+  const int rows = 128 * tree_m_tiles(max_tree, group);
+  return (max_tree * group + rows - 1) / rows;
+}
 cudaError_t launch_pool_resize(const PoolArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_slot_map(const SlotArgs &a, int sms, cudaStream_t stream);
 

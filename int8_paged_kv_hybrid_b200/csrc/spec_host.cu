@@ -36,9 +36,27 @@ int check_geometry(const hyb_pool_desc *p) {
 
 extern "C" {
 
+// Workspace of hyb_tree_attn: the partial outputs, their sums and maxima, and
+// the CTAs of every unit (TreeArgs), each part on a 256-byte boundary.
+struct TreeWs {
+  size_t o, ml, units, total;
+};
+
+static TreeWs tree_ws(const hyb_cache_desc *d, int32_t max_tree, int sms) {
+  const int group = d->num_q_heads / d->num_kv_heads;
+  const size_t rows = static_cast<size_t>(2) * sms * 128 * hyb::tree_m_tiles(max_tree, group);
+  TreeWs w;
+  w.o = 0;
+  w.ml = w.o + rows * hyb::kDim * sizeof(float);
+  w.units = w.ml + rows * 2 * sizeof(float);
+  const size_t units = static_cast<size_t>(d->batch) * d->num_kv_heads * hyb::tree_groups(max_tree, group);
+  w.total = w.units + units * sizeof(int2);
+  return w;
+}
+
 size_t hyb_tree_workspace_bytes(const hyb_cache_desc *d, int32_t max_tree) {
   if (hyb_check_desc(d) != HYB_OK || max_tree < 1 || max_tree > HYB_MAX_TREE) return 0;
-  return 16;
+  return tree_ws(d, max_tree, hyb::host_sm_count()).total;
 }
 
 int hyb_tree_attn(const hyb_cache_desc *d, const void *q, const void *k_tree, const void *v_tree,
@@ -51,9 +69,16 @@ int hyb_tree_attn(const hyb_cache_desc *d, const void *q, const void *k_tree, co
       (tree_mask && !aligned(tree_mask, 8)) || (n_tree && !aligned(n_tree, 4)) || !std::isfinite(softmax_scale))
     return HYB_ERR_INVALID_VALUE;
   if (max_tree > HYB_MAX_TREE) return HYB_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < hyb_tree_workspace_bytes(d, max_tree))
-    return HYB_ERR_WORKSPACE;
+  const int sms = hyb::host_sm_count();
+  const TreeWs w = tree_ws(d, max_tree, sms);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.total) return HYB_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   hyb::TreeArgs a;
+  a.wait_cycles = hyb::host_wait_cycles();
+  a.ctas = sms;
+  a.part_o = reinterpret_cast<float *>(ws + w.o);
+  a.part_ml = reinterpret_cast<float *>(ws + w.ml);
+  a.unit_ctas = reinterpret_cast<int2 *>(ws + w.units);
   a.hot = static_cast<const uint8_t *>(d->hot);
   a.cold = static_cast<const uint8_t *>(d->cold);
   a.scales = d->scales;

@@ -29,8 +29,9 @@ struct TreeArgs {
   int lsub;                   // log2 of the 64-token sub-blocks per block
   int bshift;                 // log2 of the tokens per block
   float qk_scale;             // softmax_scale * log2(e)
-  long long wait_cycles;      // limit (SM cycles) of the bounded waits
+  uint32_t wait_cycles;       // limit (SM cycles) of the bounded waits
   int ctas;                   // CTAs of the launch
+  int wide;                   // cold pool 32-byte aligned: 32-byte loads
   // partial results of units that several CTAs share (see tree.cu): sums and
   // maxima [2 ctas][rows], outputs [2 ctas][32][rows][4], rows = 128 * MT, and
   // the CTAs {first, last} of every unit [batch][Hkv][groups]

@@ -74,8 +74,10 @@ int hyb_tree_attn(const hyb_cache_desc *d, const void *q, const void *k_tree, co
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.total) return HYB_ERR_WORKSPACE;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   hyb::TreeArgs a;
-  a.wait_cycles = hyb::host_wait_cycles();
+  const long long wait = hyb::host_wait_cycles();
+  a.wait_cycles = wait < 0xf0000000ll ? static_cast<uint32_t>(wait) : 0xf0000000u;
   a.ctas = sms;
+  a.wide = aligned(d->cold, 32);
   a.part_o = reinterpret_cast<float *>(ws + w.o);
   a.part_ml = reinterpret_cast<float *>(ws + w.ml);
   a.unit_ctas = reinterpret_cast<int2 *>(ws + w.units);

@@ -34,7 +34,6 @@
 namespace hyb {
 
 constexpr int kTK = 128;                     // keys per tile
-constexpr int kTreeProducers = 8;            // producer warps
 constexpr int kTreeStages = 2;               // K and V tiles in shared memory
 constexpr int kTreeMeta = 4;                 // tile records (see the producers)
 constexpr uint32_t kTreeOperand = 128 * 256; // bytes of a 128 x 128 FP16 operand
@@ -42,13 +41,21 @@ constexpr uint32_t kTreeSlab = kTreeOperand / 2;  // its halves of 64 columns
 constexpr float kLagLog2 = 6.f;
 constexpr float kLagScale = 256.f;
 
+// TreeMeta::flags and TreeTile::flags
+constexpr uint32_t kTileFirst = 1, kTileLast = 2, kTileRowsShift = 2, kTileGroupShift = 4;
+
 // What the softmax needs to know of a tile; four units of 32 keys.
 struct TreeMeta {
   float k_scale[4];  // 1 for FP16 rows
   float v_scale[4];
   uint32_t ok[4];    // keys that every row attends
-  uint32_t bad[kTreeProducers][4];  // FP16 rows of a tail tile with a V that is not finite
+  uint32_t flags;    // kTileFirst, kTileLast (of its segment) and the unit's row tiles
+  uint32_t bad[4][4];  // [warp of the unit][unit]: tail rows with a V that is not finite
 };
+
+// Producer warps: with one row tile the codes set the pace; with two the MMAs
+// do, and four warps leave every thread 128 registers.
+constexpr int tree_producers(int mt) { return mt == 1 ? 8 : 4; }
 
 template <int MT>
 struct TreeSmem {
@@ -64,14 +71,15 @@ struct TreeSmem {
   uint32_t tmem;
   volatile int abort;
   int start_b;
-  long long start_base, total;
+  long long start_pos, total;  // the run's start within sequence start_b, the list's length
   long long warp_sum[32];
 };
 
 template <int MT>
 struct TreeShape {
   static constexpr int kSoftWarps = 4 * MT;
-  static constexpr int kThreads = 32 * (kSoftWarps + kTreeProducers + 1);
+  static constexpr int kProducers = tree_producers(MT);
+  static constexpr int kThreads = 32 * (kSoftWarps + kProducers + 1);
   static constexpr uint32_t kQBytes = TreeSmem<MT>::kQ * MT * kTreeOperand;
   static constexpr uint32_t kBytes = 1024 + kQBytes + 2 * kTreeStages * kTreeOperand + sizeof(TreeSmem<MT>);
 };
@@ -81,7 +89,6 @@ struct TreeShape {
 struct TreeSeq {
   int cold, hot, nt, keys;  // cold and ring tokens, nodes (rows), nodes that are keys
   int tiles, groups;        // per unit; row groups
-  long long span;           // tiles of all its units
   int status;
 };
 
@@ -102,56 +109,56 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   s.keys = bad ? 0 : s.nt;
   s.tiles = max(1, (s.cold + kTK - 1) / kTK + (s.hot + s.keys + kTK - 1) / kTK);
   s.groups = (s.nt * (a.hq / a.hkv) + 128 * MT - 1) / (128 * MT);
-  s.span = static_cast<long long>(s.tiles) * s.groups * a.hkv;
   return s;
 }
 
-// A run of tiles [w, w1) taken unit by unit.
+// A run of `left` tiles from tile `pos` of sequence b on, taken unit by unit.
 template <int MT>
 struct TreeWalk {
-  long long w, w1, base;  // base: the list's index of sequence b's first tile
-  int b;
-  TreeSeq s;
-  int hk, mg, t0, t1;     // the current segment: tiles [t0, t1) of unit (b, hk, mg)
+  long long pos;
+  int left, b;
+  int cold, tiles, groups, nt;
+  int hk, mg, t0, t1;  // the current segment: tiles [t0, t1) of unit (b, hk, mg)
 
-  __device__ __forceinline__ void init(const TreeArgs &a, long long w_, long long w1_, long long base_, int b_) {
-    w = w_;
-    w1 = w1_;
-    base = base_;
-    b = b_;
-    s = tree_seq<MT>(a, b);
+  __device__ __forceinline__ void enter(const TreeArgs &a) {
+    const TreeSeq s = tree_seq<MT>(a, b);
+    cold = s.cold;
+    tiles = s.tiles;
+    groups = s.groups;
+    nt = s.nt;
   }
   __device__ __forceinline__ bool next(const TreeArgs &a) {
-    if (w >= w1) return false;
-    while (w >= base + s.span) {
-      base += s.span;
-      s = tree_seq<MT>(a, ++b);
+    if (left == 0) return false;
+    for (;;) {
+      const long long span = static_cast<long long>(tiles) * groups * a.hkv;
+      if (pos < span) break;
+      pos -= span;
+      b++;
+      enter(a);
     }
-    const long long r = w - base;
-    const int unit = static_cast<int>(r / s.tiles);
-    t0 = static_cast<int>(r - static_cast<long long>(unit) * s.tiles);
-    t1 = static_cast<int>(min(static_cast<long long>(s.tiles), t0 + (w1 - w)));
-    hk = unit / s.groups;
-    mg = unit - hk * s.groups;
-    w += t1 - t0;
+    const int unit = static_cast<int>(pos / tiles);
+    t0 = static_cast<int>(pos - static_cast<long long>(unit) * tiles);
+    t1 = min(tiles, t0 + left);
+    hk = unit / groups;
+    mg = unit - hk * groups;
+    pos += t1 - t0;
+    left -= t1 - t0;
     return true;
   }
   // 128-row tiles of this unit that have a row
   __device__ __forceinline__ int m_tiles(const TreeArgs &a) const {
-    const int rows = s.nt * (a.hq / a.hkv) - mg * 128 * MT;
-    return MT == 1 ? 1 : min(MT, (rows + 127) / 128);
+    return MT == 1 ? 1 : min(MT, (nt * (a.hq / a.hkv) - mg * 128 * MT + 127) / 128);
   }
 };
 
 // Wait for phase `parity`; false when the wait or the kernel gave up.
 template <typename Sm>
 __device__ __forceinline__ bool tree_wait(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  if (mbar_test_wait(bar, parity)) return true;
   const bool quick = a.wait_cycles < kShortWaitCycles;
-  const long long t0 = clock64();
+  const uint32_t t0 = static_cast<uint32_t>(clock());
   while (!(quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
     if (sm.abort) return false;
-    if (clock64() - t0 > a.wait_cycles) {
+    if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
       sm.abort = 1;
       set_status(a.status, HYB_STATUS_TIMEOUT);
       return false;
@@ -199,154 +206,103 @@ __device__ __forceinline__ uint4 f16_int4(uint32_t w) {  // eight INT4 codes of 
 
 __device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
-// A producer thread's part of a tile: units u and u + 2 (u = thread / 128) of
-// 32 keys.  K: key (thread % 128) / 4, 32 channels; V: INT8 / INT4 channel
-// thread % 128, all 32 keys; FP16 channels 2 (thread % 64), + 1 and 16 keys.
-template <bool kF16>
-struct TreeRegs {
-  uint4 k[2][kF16 ? 4 : 2];
-  uint4 v[2][kF16 ? 4 : 2];
+// A producer thread has units u, u + kStep, ... of 32 keys of every tile (u =
+// thread / 128): K of key (thread % 128) / 4, 32 channels; V of INT8 / INT4
+// channel thread % 128, all 32 keys, of FP16 rows channels 2 (thread % 64), + 1
+// and 16 keys.
+template <int MT>
+struct TreePart {
+  static constexpr int kStep = tree_producers(MT) / 4;
+  static constexpr int kUnits = 4 / kStep;
 };
 
+template <int MT>
 struct TreeTile {
-  int b, hk, mg, ti;   // unit and tile; ti < 0: the list's end
-  int cold, hot, keys, nt;
-  bool first;          // of its segment
-  int ent[2];          // block-table entries of the two units (-1: none)
+  int b, hk, ti, cold;  // unit, tile (ti < 0: the list's end) and the sequence's cold tokens
+  uint32_t flags;       // as TreeMeta's, and the row group from kTileGroupShift on
+  int ent[TreePart<MT>::kUnits];  // block-table entries of the thread's units
 };
 
 template <int MT>
 struct TreeFeed {
   TreeWalk<MT> walk;
-  int t, unit0;  // next tile of the walk's segment; the thread's first unit
-  bool live;
+  int t, u;  // next tile of the walk's segment; the thread's first unit
 
-  __device__ __forceinline__ TreeTile next(const TreeArgs &a) {
-    TreeTile x;
-    bool first = false;
-    if (live && t == walk.t1) {
-      live = walk.next(a);
+  __device__ __forceinline__ TreeTile<MT> next(const TreeArgs &a) {
+    TreeTile<MT> x;
+    x.flags = 0;
+    if (t == walk.t1) {
+      if (!walk.next(a)) {
+        x.ti = -1;
+        return x;
+      }
       t = walk.t0;
-      first = true;
-    }
-    if (!live) {
-      x.ti = -1;
-      return x;
+      x.flags = kTileFirst;
     }
     x.b = walk.b;
     x.hk = walk.hk;
-    x.mg = walk.mg;
-    x.cold = walk.s.cold;
-    x.hot = walk.s.hot;
-    x.keys = walk.s.keys;
-    x.nt = walk.s.nt;
-    x.first = first;
+    x.cold = walk.cold;
     x.ti = t++;
+    if (t == walk.t1) x.flags |= kTileLast;
+    x.flags |= static_cast<uint32_t>(walk.m_tiles(a)) << kTileRowsShift;
+    x.flags |= static_cast<uint32_t>(walk.mg) << kTileGroupShift;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int p = x.ti * kTK + 32 * (unit0 + 2 * i);
+    for (int i = 0; i < TreePart<MT>::kUnits; i++) {
+      const int p = x.ti * kTK + 32 * (u + TreePart<MT>::kStep * i);
       x.ent[i] = p < x.cold ? __ldg(a.block_table + static_cast<size_t>(x.b) * a.max_blocks + (p >> a.bshift)) : -1;
     }
     return x;
   }
 };
 
-// Where unit i of a cold tile lives: valid keys (0: nothing to read).
-struct TreeUnit {
-  int n;
-  bool int4;
-  const uint8_t *base;  // the 64-token tile pair, or (FP16) the unit's first row
-  int half;             // slots 32 half .. of the tile pair
-};
-
-template <bool kF16>
-__device__ __forceinline__ TreeUnit tree_unit(const TreeArgs &a, const TreeTile &x, int i, int u) {
-  TreeUnit r;
-  const int p = x.ti * kTK + 32 * (u + 2 * i);
-  r.n = max(0, min(32, x.cold - p));
-  const int phys = x.ent[i];
-  if (r.n > 0 && (phys < 0 || phys >= a.num_phys)) {
+// Valid keys of the unit at position p of a cold tile (0: nothing to read).
+__device__ __forceinline__ int unit_keys(const TreeArgs &a, int cold, int p, int ent) {
+  const int n = max(0, min(32, cold - p));
+  if (n > 0 && (ent < 0 || ent >= a.num_phys)) {
     set_status(a.status, HYB_STATUS_BAD_BLOCK);
-    r.n = 0;
+    return 0;
   }
-  const int slot = p & ((1 << a.bshift) - 1);
-  const size_t pair = static_cast<size_t>(r.n > 0 ? phys : 0) * a.hkv + x.hk;
-  if (kF16) {
-    r.int4 = false;
-    r.half = 0;
-    r.base = a.cold + (((pair << a.bshift) + slot) * kHotTokenBytes);
-  } else {
-    r.int4 = a.quant_bits == 4 || (a.n_int4 != nullptr && (p >> a.bshift) < a.n_int4[x.b]);
-    r.half = (slot >> 5) & 1;
-    r.base = a.cold + ((pair << a.lsub) + (slot >> 6)) * kTilePairBytes;
-  }
+  return n;
+}
+
+// Codes are read once: no place in L1.
+__device__ __forceinline__ uint4 ldg16(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
   return r;
 }
-
-__device__ __forceinline__ uint4 ldg_nc(const void *p) { return __ldg(static_cast<const uint4 *>(p)); }
-
-// FP16 rows: 32 channels of the thread's key (K) ...
-__device__ __forceinline__ void rows_k(const __half *row, bool valid, int tid, uint4 (&k)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; j++)
-    k[j] = valid ? ldg_nc(row + 32 * (tid & 3) + 8 * j) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void ldg32(const void *p, uint4 &x, uint4 &y) {  // 32-byte aligned
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+               : "l"(p));
 }
 
-// ... and two channels of 16 keys (V); row(j) is the V row of key j or null.
-template <typename Row>
-__device__ __forceinline__ void rows_v(Row row, int tid, uint4 (&v)[4]) {
-  uint32_t *w = reinterpret_cast<uint32_t *>(v);
-  const int k0 = 16 * ((tid >> 6) & 1), c = 2 * (tid & 63);
-#pragma unroll
-  for (int j = 0; j < 16; j++) {
-    const __half *r = row(k0 + j);
-    w[j] = r ? __ldg(reinterpret_cast<const uint32_t *>(r + c)) : 0u;
-  }
-}
-
-template <bool kF16>
-__device__ __forceinline__ void load_cold_k(const TreeUnit &n, int tid, uint4 (&k)[kF16 ? 4 : 2]) {
-  const int key = (tid & 127) >> 2;
-  if constexpr (kF16) {
-    rows_k(reinterpret_cast<const __half *>(n.base) + key * 2 * kDim, key < n.n, tid, k);
+// Codes of a unit: the thread's 32 bytes (INT4: 16) of K or V of the 64-token
+// tile pair at `pair` that holds the unit as slots 32 half ...
+__device__ __forceinline__ void load_codes(const TreeArgs &a, const uint8_t *p, uint4 (&r)[2]) {
+  if (a.wide) {
+    ldg32(p, r[0], r[1]);
   } else {
-    k[0] = k[1] = make_uint4(0, 0, 0, 0);
-    if (n.n == 0) return;
-    const int slot = 32 * n.half + key;
-    if (n.int4) {
-      k[0] = ldg_nc(n.base + slot * 64 + 16 * (tid & 3));
-    } else {
-      k[0] = ldg_nc(n.base + slot * 128 + 32 * (tid & 3));
-      k[1] = ldg_nc(n.base + slot * 128 + 32 * (tid & 3) + 16);
-    }
+    r[0] = ldg16(p);
+    r[1] = ldg16(p + 16);
   }
 }
 
-template <bool kF16>
-__device__ __forceinline__ void load_cold_v(const TreeUnit &n, int tid, uint4 (&v)[kF16 ? 4 : 2]) {
-  if constexpr (kF16) {
-    const __half *base = reinterpret_cast<const __half *>(n.base) + kDim;
-    rows_v([&](int j) { return j < n.n ? base + j * 2 * kDim : nullptr; }, tid, v);
-  } else {
-    v[0] = v[1] = make_uint4(0, 0, 0, 0);
-    if (n.n == 0) return;
-    // the unit's two 16-slot chunks are one aligned pair, swapped where the
-    // swizzle's lowest bit is set: v[0] is slots 0..15, v[1] 16..31 (INT4:
-    // words 0, 1 and 2, 3 of v[0])
-    const int c = tid & 127;
-    const uint8_t *t = n.base + kTileBytes;
-    if (n.int4) {
-      const int x = (c >> 2) & 3;
-      const uint4 y = ldg_nc(t + c * 32 + 8 * ((2 * n.half) ^ (x & 2)));
-      v[0] = x & 1 ? make_uint4(y.z, y.w, y.x, y.y) : y;
-    } else {
-      const int x = (c >> 1) & 3;
-      const uint8_t *p = t + c * 64 + 16 * ((2 * n.half) ^ (x & 2));
-      const uint4 y = ldg_nc(p), z = ldg_nc(p + 16);
-      v[0] = x & 1 ? z : y;
-      v[1] = x & 1 ? y : z;
-    }
-  }
+__device__ __forceinline__ void load_k(const TreeArgs &a, const uint8_t *pair, int half, bool int4, int tid, uint4 (&k)[2]) {
+  const int slot = 32 * half + ((tid & 127) >> 2);
+  if (int4) k[0] = ldg16(pair + slot * 64 + 16 * (tid & 3));
+  else load_codes(a, pair + slot * 128 + 32 * (tid & 3), k);
+}
+
+// (V: the unit's two 16-slot chunks are one aligned pair, swapped where the
+// swizzle's lowest bit is set; store_v8 puts them right)
+__device__ __forceinline__ void load_v(const TreeArgs &a, const uint8_t *pair, int half, bool int4, int tid, uint4 (&v)[2]) {
+  const int c = tid & 127;
+  const uint8_t *t = pair + kTileBytes;
+  if (int4) v[0] = ldg16(t + c * 32 + 8 * ((2 * half) ^ ((c >> 2) & 2)));
+  else load_codes(a, t + c * 64 + 16 * ((2 * half) ^ ((c >> 1) & 2)), v);
 }
 
 // K of one unit into the operand: row = key, 32 channels = four 16-byte chunks
@@ -385,25 +341,30 @@ __device__ __forceinline__ void store_k8(uint32_t st, int u, int tid, bool int4,
 __device__ __forceinline__ void store_v8(uint32_t st, int u, int tid, bool int4, const uint4 (&v)[2]) {
   const int row = tid & 127;
   const uint32_t base = st + (u >> 1) * kTreeSlab + row * 128;
-  const int c = 4 * (u & 1), x = row & 7;
+  const int c = 4 * (u & 1);
   if (int4) {
+    // the swap, as a bit of the chunk
+    const int x = (row & 7) ^ ((row >> 2 & 1) << 1);
     sts128(base + (((c + 0) ^ x) << 4), f16_int4(v[0].x));
     sts128(base + (((c + 1) ^ x) << 4), f16_int4(v[0].y));
     sts128(base + (((c + 2) ^ x) << 4), f16_int4(v[0].z));
     sts128(base + (((c + 3) ^ x) << 4), f16_int4(v[0].w));
   } else {
-    sts128(base + (((c + 0) ^ x) << 4), f16_int8(v[0].x, v[0].y));
-    sts128(base + (((c + 1) ^ x) << 4), f16_int8(v[0].z, v[0].w));
-    sts128(base + (((c + 2) ^ x) << 4), f16_int8(v[1].x, v[1].y));
-    sts128(base + (((c + 3) ^ x) << 4), f16_int8(v[1].z, v[1].w));
+    // (here that would leave eight rows four places: the words swap)
+    const int x = row & 7;
+    const bool swap = row & 2;
+    const uint4 y = swap ? v[1] : v[0], z = swap ? v[0] : v[1];
+    sts128(base + (((c + 0) ^ x) << 4), f16_int8(y.x, y.y));
+    sts128(base + (((c + 1) ^ x) << 4), f16_int8(y.z, y.w));
+    sts128(base + (((c + 2) ^ x) << 4), f16_int8(z.x, z.y));
+    sts128(base + (((c + 3) ^ x) << 4), f16_int8(z.z, z.w));
   }
 }
 
 // FP16 V of one unit: the thread's two channels are two rows, its 16 keys two
 // chunks of each.  Lanes 4..7 of eight write their odd row first, so that the
 // eight rows differ modulo 8.
-__device__ __forceinline__ void store_v16(uint32_t st, int u, int tid, const uint4 (&v)[4]) {
-  const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+__device__ __forceinline__ void store_v16(uint32_t st, int u, int tid, const uint32_t (&w)[16]) {
   const int p = tid & 63, odd = (p >> 2) & 1;
   const int c0 = 4 * (u & 1) + 2 * ((tid >> 6) & 1);
 #pragma unroll
@@ -421,175 +382,215 @@ __device__ __forceinline__ void store_v16(uint32_t st, int u, int tid, const uin
   }
 }
 
-// Row r of the tail (ring rows in the order of their positions, then nodes):
-// its K row (V row: + add), or null.
-__device__ __forceinline__ const __half *tail_row(const TreeArgs &a, const TreeTile &x, int r, int kv) {
-  if (r < x.hot) {
-    const int slot = (x.cold + r) & (a.hot_tokens - 1);
-    return reinterpret_cast<const __half *>(a.hot) +
-           (((static_cast<size_t>(x.b) * a.hkv + x.hk) * a.hot_tokens + slot) * 2 + kv) * kDim;
+// FP16 rows as units: rows of an FP16 cold block (`base`, n of them valid), or
+// rows r0.. of the tail (the ring's in the order of their positions, then the
+// nodes).
+struct TreeRows {
+  const __half *base;  // null: the tail
+  int n;
+  int b, hk, cold, hot, keys, r0;
+
+  // the K row (kv 1: V row) of key k of the unit, or null
+  __device__ __forceinline__ const __half *row(const TreeArgs &a, int k, int kv) const {
+    if (base) return k < n ? base + (2 * k + kv) * kDim : nullptr;
+    int r = r0 + k;
+    if (r < hot)
+      return reinterpret_cast<const __half *>(a.hot) +
+             (((static_cast<size_t>(b) * a.hkv + hk) * a.hot_tokens + ((cold + r) & (a.hot_tokens - 1))) * 2 + kv) * kDim;
+    r -= hot;
+    if (r >= keys) return nullptr;
+    return (kv ? a.v_tree : a.k_tree) + ((static_cast<size_t>(b) * a.max_tree + r) * a.hkv + hk) * kDim;
   }
-  r -= x.hot;
-  if (r >= x.keys) return nullptr;
-  return (kv ? a.v_tree : a.k_tree) + ((static_cast<size_t>(x.b) * a.max_tree + r) * a.hkv + x.hk) * kDim;
+};
+
+__device__ __forceinline__ void rows_k(const TreeArgs &a, const TreeRows &x, int tid, uint4 (&k)[4]) {
+  const __half *row = x.row(a, (tid & 127) >> 2, 0);
+#pragma unroll
+  for (int j = 0; j < 4; j++) k[j] = row ? ldg16(row + 32 * (tid & 3) + 8 * j) : make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void rows_v(const TreeArgs &a, const TreeRows &x, int tid, uint32_t (&w)[16]) {
+  const int k0 = 16 * ((tid >> 6) & 1), c = 2 * (tid & 63);
+#pragma unroll
+  for (int j = 0; j < 16; j++) {
+    const __half *r = x.row(a, k0 + j, 1);
+    w[j] = r ? __ldg(reinterpret_cast<const uint32_t *>(r + c)) : 0u;
+  }
 }
 
 // The query rows of a unit into its Q operand(s); rows beyond the tree are 0.
 template <int MT>
-__device__ __forceinline__ void load_q(const TreeArgs &a, const TreeTile &x, uint32_t st, int tid) {
-  const int G = a.hq / a.hkv, rows = x.nt * G;
+__device__ __forceinline__ void load_q(const TreeArgs &a, const TreeTile<MT> &x, uint32_t st, int tid) {
+  const int G = a.hq / a.hkv, mg = x.flags >> kTileGroupShift;
+  const int rows = (a.n_tree ? a.n_tree[x.b] : a.max_tree) * G;
 #pragma unroll 4
-  for (int i = tid; i < 128 * MT * 16; i += 32 * kTreeProducers) {
-    const int r = i >> 4, c = i & 15, row = x.mg * 128 * MT + r;
+  for (int i = tid; i < 128 * MT * 16; i += 32 * tree_producers(MT)) {
+    const int r = i >> 4, c = i & 15, row = mg * 128 * MT + r;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (row < rows) {
       const int t = row / G;
-      v = ldg_nc(a.q + ((static_cast<size_t>(x.b) * a.max_tree + t) * a.hq + x.hk * G + row - t * G) * kDim + 8 * c);
+      v = ldg16(a.q + ((static_cast<size_t>(x.b) * a.max_tree + t) * a.hq + x.hk * G + row - t * G) * kDim + 8 * c);
     }
     sts128(st + (r >> 7) * kTreeOperand + (c >> 3) * kTreeSlab + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4), v);
   }
 }
 
+// (The MMA thread orders these writes before its MMAs with one proxy fence: a
+// fence here would wait for the thread's loads in flight.)
 __device__ __forceinline__ void producer_arrive(uint64_t *bar, int lane) {
-  fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
 
 template <int MT, bool kF16>
 __device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s,
-                                             uint32_t v_s, long long w0, long long w1) {
-  const int tid = threadIdx.x - 32 * TreeShape<MT>::kSoftWarps, lane = tid & 31, warp = tid >> 5;
+                                             uint32_t v_s, int n) {
+  const int tid = threadIdx.x - 32 * TreeShape<MT>::kSoftWarps, lane = tid & 31;
   const int u = tid >> 7;
-  constexpr int kQ = TreeSmem<MT>::kQ;
+  constexpr int kQ = TreeSmem<MT>::kQ, kUnits = TreePart<MT>::kUnits, kStep = TreePart<MT>::kStep;
   TreeFeed<MT> feed;
-  feed.walk.init(a, w0, w1, sm.start_base, sm.start_b);
-  feed.walk.t1 = 0;
-  feed.t = 0;
-  feed.unit0 = u;
-  feed.live = true;
-  TreeTile cur = feed.next(a), nxt = feed.next(a);
-  TreeRegs<kF16> regs;
-  TreeUnit un[2];
-  float2 sc[2];  // the units' scales (thread 0 of each half writes the records)
+  feed.walk.pos = sm.start_pos;
+  feed.walk.left = n;
+  feed.walk.b = sm.start_b;
+  feed.walk.enter(a);
+  feed.walk.t1 = feed.t = 0;
+  feed.u = u;
+  TreeTile<MT> cur, nxt = feed.next(a);
+  cur.ti = -1;
+  cur.cold = 0;
   const bool scribe = (tid & 127) == 0;
+  // of the tile whose codes are in registers: codes, scales, valid keys, formats
+  uint4 rk[kF16 ? 1 : kUnits][2], rv[kF16 ? 1 : kUnits][2];
+  float2 sc[kUnits];
+  int valid[kUnits];
+  uint32_t fmt = 0, fmt_next = 0;  // bit i: unit i is INT4
 
-  auto is_cold = [&](const TreeTile &x) { return x.ti >= 0 && x.ti * kTK < x.cold; };
-  auto units = [&](const TreeTile &x) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      un[i] = tree_unit<kF16>(a, x, i, u);
-      sc[i] = kF16 ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f);
-      if (!kF16 && scribe && un[i].n > 0)
-        sc[i] = __ldg(reinterpret_cast<const float2 *>(a.scales) + static_cast<size_t>(x.ent[i]) * a.hkv + x.hk);
-    }
-  };
-  if (is_cold(cur)) {
-    units(cur);
-#pragma unroll
-    for (int i = 0; i < 2; i++) load_cold_k<kF16>(un[i], tid, regs.k[i]);
-#pragma unroll
-    for (int i = 0; i < 2; i++) load_cold_v<kF16>(un[i], tid, regs.v[i]);
-  }
+  // one round per tile, and one before the first that only loads
   int seg = -1;
-  for (int j = 0; cur.ti >= 0; j++) {
-    const int s = j % kTreeStages;
+  for (int j = -1; j < n; j++) {
+    const int s = j & (kTreeStages - 1);
     const uint32_t ph = (j / kTreeStages) & 1;
-    const TreeTile nn = feed.next(a);
-    if (cur.first) {
-      seg++;
-      if (!tree_wait_warp(sm, &sm.qempty[seg % kQ], ((seg / kQ) & 1) ^ 1, a)) return;
-      load_q<MT>(a, cur, q_s + (seg % kQ) * MT * kTreeOperand, tid);
-      producer_arrive(&sm.qfull[seg % kQ], lane);
-    }
     const uint32_t kst = k_s + s * kTreeOperand, vst = v_s + s * kTreeOperand;
-    TreeMeta &m = sm.meta[j % kTreeMeta];
-    if (is_cold(cur)) {
-      if (!tree_wait_warp(sm, &sm.kempty[s], ph ^ 1, a)) return;
-      const bool int4[2] = {un[0].int4, un[1].int4};
+    const bool cold = j >= 0 && cur.ti * kTK < cur.cold;
+    const TreeTile<MT> nn = feed.next(a);
+    if (j >= 0) {
+      if (cur.flags & kTileFirst) {
+        seg++;
+        if (!tree_wait_warp(sm, &sm.qempty[seg % kQ], ((seg / kQ) & 1) ^ 1, a)) return;
+        load_q<MT>(a, cur, q_s + (seg % kQ) * MT * kTreeOperand, tid);
+        producer_arrive(&sm.qfull[seg % kQ], lane);
+      }
+      TreeMeta &m = sm.meta[j & (kTreeMeta - 1)];
+      uint32_t bad = 0;  // lane c < 4: unit c
+      if (kF16 || !cold) {
+        // FP16 rows.  V first: the record names the nodes whose V is not
+        // finite.  Such a value must not meet the zero weight of a row that
+        // does not attend its node: it becomes 0 here, and the rows that do
+        // attend the node add it at the end
+        const TreeSeq q = tree_seq<MT>(a, cur.b);
+        const int tail0 = (cur.ti - (cur.cold + kTK - 1) / kTK) * kTK;
+        auto rows = [&](int i) {
+          const int c = u + kStep * i;
+          TreeRows x{nullptr, 0, cur.b, cur.hk, cur.cold, q.hot, q.keys, tail0 + 32 * c};
+          if (kF16 && cold) {
+            const int p = cur.ti * kTK + 32 * c;
+            x.n = unit_keys(a, cur.cold, p, cur.ent[i]);
+            x.base = reinterpret_cast<const __half *>(
+                a.cold + ((((static_cast<size_t>(x.n ? cur.ent[i] : 0) * a.hkv + cur.hk) << a.bshift) +
+                           (p & ((1 << a.bshift) - 1))) * kHotTokenBytes));
+          }
+          return x;
+        };
+        if (!tree_wait_warp(sm, &sm.vempty[s], ph ^ 1, a)) return;
+#pragma unroll
+        for (int i = 0; i < kUnits; i++) {
+          const int c = u + kStep * i, k0 = 16 * ((tid >> 6) & 1);
+          const TreeRows x = rows(i);
+          uint32_t w[16];
+          rows_v(a, x, tid, w);
+          if (!(kF16 && cold)) {
+            uint32_t b = 0;
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+              if (x.r0 + k0 + k < q.hot) continue;
+              const bool lo = f16_not_finite(w[k]), hi = f16_not_finite(w[k] >> 16);
+              if (lo) w[k] &= 0xffff0000u;
+              if (hi) w[k] &= 0x0000ffffu;
+              if (lo || hi) b |= 1u << (k0 + k);
+            }
+            b = __reduce_or_sync(0xffffffffu, b);
+            if (lane == c) bad = b;
+          }
+          store_v16(vst, c, tid, w);
+          sc[i] = make_float2(1.f, 1.f);
+          valid[i] = kF16 && cold ? x.n : max(0, min(32, q.hot - x.r0));
+        }
+        producer_arrive(&sm.vfull[s], lane);
+        if (!tree_wait_warp(sm, &sm.kempty[s], ph ^ 1, a)) return;
+#pragma unroll
+        for (int i = 0; i < kUnits; i++) {
+          uint4 k[4];
+          rows_k(a, rows(i), tid, k);
+          store_k16(kst, u + kStep * i, tid, k);
+        }
+      } else {
+        if (!tree_wait_warp(sm, &sm.kempty[s], ph ^ 1, a)) return;
+        if constexpr (!kF16) {
+#pragma unroll
+          for (int i = 0; i < kUnits; i++) store_k8(kst, u + kStep * i, tid, fmt >> i & 1, rk[i]);
+        }
+      }
+      if (lane < 4 && lane % kStep == u) m.bad[(tid >> 5) & 3][lane] = bad;
       if (scribe) {
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          m.k_scale[u + 2 * i] = sc[i].x;
-          m.v_scale[u + 2 * i] = sc[i].y;
-          m.ok[u + 2 * i] = un[i].n >= 32 ? 0xffffffffu : (1u << un[i].n) - 1;
+        for (int i = 0; i < kUnits; i++) {
+          const int c = u + kStep * i;
+          m.k_scale[c] = sc[i].x;
+          m.v_scale[c] = sc[i].y;
+          m.ok[c] = valid[i] >= 32 ? 0xffffffffu : (1u << valid[i]) - 1;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        if constexpr (kF16) store_k16(kst, u + 2 * i, tid, regs.k[i]);
-        else store_k8(kst, u + 2 * i, tid, int4[i], regs.k[i]);
+        if (u == 0) m.flags = cur.flags;
       }
       producer_arrive(&sm.kfull[s], lane);
-      if (lane == 0) mbar_arrive(&sm.mfull[j % kTreeMeta]);
-      if (is_cold(nxt)) {
-        units(nxt);
+      if (lane == 0) mbar_arrive(&sm.mfull[j & (kTreeMeta - 1)]);
+    }
+    // the next tile's codes are on their way while this one's V is stored
+    const bool more = !kF16 && nxt.ti >= 0 && nxt.ti * kTK < nxt.cold;
+    const uint8_t *pair[kUnits];
+    if (!kF16 && more) {
+      fmt_next = 0;
 #pragma unroll
-        for (int i = 0; i < 2; i++) load_cold_k<kF16>(un[i], tid, regs.k[i]);
-      }
-      if (!tree_wait_warp(sm, &sm.vempty[s], ph ^ 1, a)) return;
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        if constexpr (kF16) store_v16(vst, u + 2 * i, tid, regs.v[i]);
-        else store_v8(vst, u + 2 * i, tid, int4[i], regs.v[i]);
-      }
-      producer_arrive(&sm.vfull[s], lane);
-      if (is_cold(nxt)) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) load_cold_v<kF16>(un[i], tid, regs.v[i]);
-      }
-    } else {
-      // ring rows and nodes: at most two of a unit's tiles
-      const int r0 = (cur.ti - (cur.cold + kTK - 1) / kTK) * kTK;
-      uint4 tk[2][4], tv[2][4];
-      uint32_t bad[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int ru = r0 + 32 * (u + 2 * i);
-        const __half *row = tail_row(a, cur, ru + ((tid & 127) >> 2), 0);
-        rows_k(row, row != nullptr, tid, tk[i]);
-        rows_v([&](int k) { return tail_row(a, cur, ru + k, 1); }, tid, tv[i]);
-        // a V that is not finite must not meet the zero weight of a row that
-        // does not attend it: it becomes 0 here, and the rows that do attend
-        // the node add it at the end
-        uint32_t *w = reinterpret_cast<uint32_t *>(tv[i]);
-#pragma unroll
-        for (int k = 0; k < 16; k++) {
-          const int r = 16 * ((tid >> 6) & 1) + k;
-          if (ru + r < cur.hot) continue;
-          const bool lo = f16_not_finite(w[k]), hi = f16_not_finite(w[k] >> 16);
-          if (lo) w[k] &= 0xffff0000u;
-          if (hi) w[k] &= 0x0000ffffu;
-          if (lo || hi) bad[i] |= 1u << r;
-        }
-        bad[i] = __reduce_or_sync(0xffffffffu, bad[i]);
-      }
-      if (!tree_wait_warp(sm, &sm.kempty[s], ph ^ 1, a)) return;
-      if (lane < 4) m.bad[warp][lane] = (lane & 1) == u ? bad[lane >> 1] : 0u;
-      if (scribe) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int n = max(0, min(32, cur.hot - (r0 + 32 * (u + 2 * i))));
-          m.k_scale[u + 2 * i] = 1.f;
-          m.v_scale[u + 2 * i] = 1.f;
-          m.ok[u + 2 * i] = n >= 32 ? 0xffffffffu : (1u << n) - 1;
+      for (int i = 0; i < kUnits; i++) {
+        const int p = nxt.ti * kTK + 32 * (u + kStep * i);
+        valid[i] = unit_keys(a, nxt.cold, p, nxt.ent[i]);
+        const bool int4 = a.quant_bits == 4 || (a.n_int4 != nullptr && (p >> a.bshift) < a.n_int4[nxt.b]);
+        if (int4) fmt_next |= 1u << i;
+        const int slot = p & ((1 << a.bshift) - 1);
+        const size_t at = static_cast<size_t>(valid[i] ? nxt.ent[i] : 0) * a.hkv + nxt.hk;
+        pair[i] = a.cold + ((at << a.lsub) + (slot >> 6)) * kTilePairBytes;
+        // (an empty unit has code 0 and no say in the reference scale)
+        sc[i] = make_float2(0.f, 0.f);
+        rk[i][0] = rk[i][1] = make_uint4(0, 0, 0, 0);
+        if (valid[i]) {
+          load_k(a, pair[i], (slot >> 5) & 1, int4, tid, rk[i]);
+          if (scribe) sc[i] = __ldg(reinterpret_cast<const float2 *>(a.scales) + at);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; i++) store_k16(kst, u + 2 * i, tid, tk[i]);
-      producer_arrive(&sm.kfull[s], lane);
-      if (lane == 0) mbar_arrive(&sm.mfull[j % kTreeMeta]);
+    }
+    if (!kF16 && cold) {
       if (!tree_wait_warp(sm, &sm.vempty[s], ph ^ 1, a)) return;
 #pragma unroll
-      for (int i = 0; i < 2; i++) store_v16(vst, u + 2 * i, tid, tv[i]);
+      for (int i = 0; i < kUnits; i++) store_v8(vst, u + kStep * i, tid, fmt >> i & 1, rv[i]);
       producer_arrive(&sm.vfull[s], lane);
-      if (is_cold(nxt)) {
-        units(nxt);
+    }
+    if (!kF16 && more) {
 #pragma unroll
-        for (int i = 0; i < 2; i++) load_cold_k<kF16>(un[i], tid, regs.k[i]);
-#pragma unroll
-        for (int i = 0; i < 2; i++) load_cold_v<kF16>(un[i], tid, regs.v[i]);
+      for (int i = 0; i < kUnits; i++) {
+        const int p = nxt.ti * kTK + 32 * (u + kStep * i);
+        rv[i][0] = rv[i][1] = make_uint4(0, 0, 0, 0);
+        if (valid[i]) load_v(a, pair[i], (p & ((1 << a.bshift) - 1)) >> 5 & 1, fmt_next >> i & 1, tid, rv[i]);
       }
+      fmt = fmt_next;
     }
     cur = nxt;
     nxt = nn;
@@ -601,226 +602,224 @@ __device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm
 // 128 m, O at 256 + 128 m.  The weights of a tile replace its S (FP16, the
 // first 64 columns).
 
+// S of tile j, row tile m
+template <int MT>
+__device__ __forceinline__ void tree_qk(TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t tmem, int j, int seg, int m) {
+  const int buf = MT == 1 ? j & 1 : m;
+  const uint64_t dq = tc_desc_sw128(q_s + ((seg % TreeSmem<MT>::kQ) * MT + m) * kTreeOperand);
+  const uint64_t dk = tc_desc_sw128(k_s + (j & (kTreeStages - 1)) * kTreeOperand);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint64_t o = (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3);
+    tc_mma_ss(tmem + 128 * buf, dq + o, dk + o, tc_idesc_f16(128), i > 0);
+  }
+  tc_commit(&sm.sfull[buf]);
+}
+
+// O += P V of tile j, row tile m, whose n-th tile it is
+template <int MT>
+__device__ __forceinline__ bool tree_pv(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t v_s, uint32_t tmem, int j, int m,
+                                        int n, bool first) {
+  const int buf = MT == 1 ? n & 1 : m;
+  if (!tree_wait(sm, &sm.pfull[buf], (MT == 1 ? n >> 1 : n) & 1, a)) return false;
+  if (!tree_wait(sm, &sm.vfull[j & (kTreeStages - 1)], (j / kTreeStages) & 1, a)) return false;
+  fence_proxy_async_smem();
+  tc_fence_after();
+  const uint64_t dv = tc_desc_sw128(v_s + (j & (kTreeStages - 1)) * kTreeOperand);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint64_t o = (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3);
+    tc_mma_ts(tmem + 256 + 128 * m, tmem + 128 * buf + 8 * i, dv + o, tc_idesc_f16(128), !first || i > 0);
+  }
+  tc_commit(&sm.odone[m][n & 1]);
+  return true;
+}
+
 template <int MT>
 __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
-                                         uint32_t tmem, long long w0, long long w1) {
-  constexpr uint32_t idesc = tc_idesc_f16(128);
+                                         uint32_t tmem, int n) {
   constexpr int kQ = TreeSmem<MT>::kQ;
-  TreeWalk<MT> wq, wp;  // the walks of Q K^T (one tile ahead) and of P V
-  wq.init(a, w0, w1, sm.start_base, sm.start_b);
-  wp.init(a, w0, w1, sm.start_base, sm.start_b);
-  const int n = static_cast<int>(w1 - w0);
-  int seg_q = -1, left_q = 0, mt_q = 0, jq = 0;  // jq: tiles whose Q K^T is issued
-  int used[2] = {0, 0};                          // tiles of row tile m issued (MT 2), for its barriers' phases
-  int seg_o[2] = {0, 0};                         // segments of row tile m begun
+  int seg = -1;                           // of the last tile opened
+  uint32_t flags_q = 0, flags_p;          // of the tiles of Q K^T (one ahead) and of P V
+  int used0 = 0, used1 = 0, o0 = 0, o1 = 0;  // tiles and segments of row tiles 0 and 1
 
-  // make tile jq ready: its segment's Q and its K
-  auto open = [&]() -> bool {
-    if (left_q == 0) {
-      wq.next(a);
-      seg_q++;
-      left_q = wq.t1 - wq.t0;
-      mt_q = wq.m_tiles(a);
-      if (!tree_wait(sm, &sm.qfull[seg_q % kQ], (seg_q / kQ) & 1, a)) return false;
+  // tile j's K is there, and its segment's Q
+  auto open = [&](int j) -> bool {
+    if (!tree_wait(sm, &sm.kfull[j & (kTreeStages - 1)], (j / kTreeStages) & 1, a)) return false;
+    flags_q = sm.meta[j & (kTreeMeta - 1)].flags;
+    if (flags_q & kTileFirst) {
+      seg++;
+      if (!tree_wait(sm, &sm.qfull[seg % kQ], (seg / kQ) & 1, a)) return false;
     }
-    return tree_wait(sm, &sm.kfull[jq % kTreeStages], (jq / kTreeStages) & 1, a);
-  };
-  auto qk = [&](int m) {
+    fence_proxy_async_smem();
     tc_fence_after();
-    const uint32_t q = q_s + ((seg_q % kQ) * MT + m) * kTreeOperand, k = k_s + (jq % kTreeStages) * kTreeOperand;
-    const int buf = MT == 1 ? jq & 1 : m;
-    const uint64_t dq = tc_desc_sw128(q), dk = tc_desc_sw128(k);
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const uint64_t o = (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3);
-      tc_mma_ss(tmem + 128 * buf, dq + o, dk + o, idesc, i > 0);
-    }
-    tc_commit(&sm.sfull[buf]);
-  };
-  auto close = [&]() {
-    tc_commit(&sm.kempty[jq % kTreeStages]);
-    if (--left_q == 0) tc_commit(&sm.qempty[seg_q % kQ]);
-    jq++;
-  };
-  auto pv = [&](int j, int m, bool first) -> bool {
-    const int buf = MT == 1 ? j & 1 : m;
-    const uint32_t ph = MT == 1 ? (j >> 1) & 1 : used[m] & 1;
-    if (first) {
-      if (!tree_wait(sm, &sm.ofree[m], (seg_o[m] & 1) ^ 1, a)) return false;
-      seg_o[m]++;
-    }
-    if (!tree_wait(sm, &sm.pfull[buf], ph, a)) return false;
-    if (!tree_wait(sm, &sm.vfull[j % kTreeStages], (j / kTreeStages) & 1, a)) return false;
-    tc_fence_after();
-    const uint64_t dv = tc_desc_sw128(v_s + (j % kTreeStages) * kTreeOperand);
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const uint64_t o = (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3);
-      tc_mma_ts(tmem + 256 + 128 * m, tmem + 128 * buf + 8 * i, dv + o, idesc, !first || i > 0);
-    }
-    tc_commit(&sm.odone[m][used[m] & 1]);
-    used[m]++;
     return true;
   };
+  auto close = [&](int j) {
+    tc_commit(&sm.kempty[j & (kTreeStages - 1)]);
+    if (flags_q & kTileLast) tc_commit(&sm.qempty[seg % kQ]);
+  };
+  auto two = [](uint32_t flags) { return MT == 2 && ((flags >> kTileRowsShift) & 3) == 2; };
 
-  if (n > 0) {
-    if (!open()) return;
-    for (int m = 0; m < mt_q; m++) qk(m);
-    close();
-  }
-  int left_p = 0, mt_p = 0;
-  bool first = false;
+  if (!open(0)) return;
+  tree_qk<MT>(sm, q_s, k_s, tmem, 0, seg, 0);
+  if (two(flags_q)) tree_qk<MT>(sm, q_s, k_s, tmem, 0, seg, 1);
+  close(0);
   for (int j = 0; j < n; j++) {
-    if (left_p == 0) {
-      wp.next(a);
-      left_p = wp.t1 - wp.t0;
-      mt_p = wp.m_tiles(a);
-      first = true;
+    flags_p = flags_q;
+    const bool more = j + 1 < n, first = flags_p & kTileFirst;
+    if (first) {
+      if (!tree_wait(sm, &sm.ofree[0], (o0++ & 1) ^ 1, a)) return;
+      if (two(flags_p) && !tree_wait(sm, &sm.ofree[1], (o1++ & 1) ^ 1, a)) return;
     }
-    const bool more = j + 1 < n;
     if (MT == 1) {
       if (more) {
-        if (!open()) return;
-        qk(0);
-        close();
+        if (!open(j + 1)) return;
+        tree_qk<MT>(sm, q_s, k_s, tmem, j + 1, seg, 0);
+        close(j + 1);
       }
-      if (!pv(j, 0, first)) return;
+      if (!tree_pv<MT>(a, sm, v_s, tmem, j, 0, used0++, first)) return;
     } else {
       // the next tile's S of a row tile follows that row tile's P V, whose
-      // weights it overwrites; a row tile idle in this segment is free at once
-      bool opened = false;
-      for (int m = 0; m < MT; m++) {
-        if (m < mt_p && !pv(j, m, first)) return;
-        if (more) {
-          if (!opened && !open()) return;
-          opened = true;
-          if (m < mt_q) qk(m);
-        }
+      // weights it overwrites
+      if (!tree_pv<MT>(a, sm, v_s, tmem, j, 0, used0++, first)) return;
+      if (more) {
+        if (!open(j + 1)) return;
+        tree_qk<MT>(sm, q_s, k_s, tmem, j + 1, seg, 0);
       }
-      if (more) close();
+      if (two(flags_p) && !tree_pv<MT>(a, sm, v_s, tmem, j, 1, used1++, first)) return;
+      if (more) {
+        if (two(flags_q)) tree_qk<MT>(sm, q_s, k_s, tmem, j + 1, seg, 1);
+        close(j + 1);
+      }
     }
-    tc_commit(&sm.vempty[j % kTreeStages]);
-    left_p--;
-    first = false;
+    tc_commit(&sm.vempty[j & (kTreeStages - 1)]);
   }
 }
 
 // ---- softmax ----
 
-__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t *v) {
   float m[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) m[k] = __uint_as_float(v[k]);
 #pragma unroll
-  for (int k = 4; k < 32; k++) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(v[k]));
+  for (int k = 4; k < N; k++) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(v[k]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// Keys of unit c of a tile that the row attends (bits): the record's, and in a
+// tail tile the nodes the row's mask names; `odd` collects the attended nodes
+// whose V is not finite.  k: the node of the unit's first key.
+__device__ __forceinline__ uint32_t tree_ok(const TreeMeta &me, int c, bool tail, int k, uint64_t nodes, uint64_t &odd) {
+  uint32_t ok = me.ok[c];
+  if (tail) {
+    uint32_t own = 0, bad = 0;
+    if (k >= 0) own = k < 64 ? static_cast<uint32_t>(nodes >> k) : 0u;
+    else if (k > -32) own = static_cast<uint32_t>(nodes << -k);
+#pragma unroll
+    for (int w = 0; w < 4; w++) bad |= me.bad[w][c];
+    bad &= own;
+    if (bad) odd |= k >= 0 ? static_cast<uint64_t>(bad) << k : static_cast<uint64_t>(bad) >> -k;
+    ok |= own;
+  }
+  return ok;
+}
+
 template <int MT>
-__device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t tmem, long long w0,
-                                             long long w1) {
+__device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t tmem, int n_tiles) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mt = warp >> 2, row_in = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t t_o = tmem + lanes + 256 + 128 * mt;
-  const int G = a.hq / a.hkv, groups_max = (a.max_tree * G + 128 * MT - 1) / (128 * MT);
+  const int G = a.hq / a.hkv;
   TreeWalk<MT> walk;
-  walk.init(a, w0, w1, sm.start_base, sm.start_b);
+  walk.pos = sm.start_pos;
+  walk.left = n_tiles;
+  walk.b = sm.start_b;
+  walk.enter(a);
   int j = 0;      // tiles of the CTA so far
   int mine = 0;   // tiles of this row tile so far
   while (walk.next(a)) {
-    const int n = walk.t1 - walk.t0;
     if (MT > 1 && mt >= walk.m_tiles(a)) {
-      j += n;
+      j += walk.t1 - walk.t0;
       continue;
     }
     const int row = walk.mg * 128 * MT + mt * 128 + row_in;
-    const bool live = row < walk.s.nt * G;
-    const bool warp_live = row - lane < walk.s.nt * G;
+    const bool live = row < walk.nt * G;
+    const bool warp_live = row - lane < walk.nt * G;
     const int t = live ? row / G : 0;
+    const int cold_tiles = (walk.cold + kTK - 1) / kTK;
     uint64_t nodes = 0;  // nodes this row attends
-    if (live && walk.s.keys > 0) {
-      nodes = a.mask ? a.mask[static_cast<size_t>(walk.b) * a.max_tree + t] : (~0ull >> (63 - t));
-      if (walk.s.keys < 64) nodes &= (1ull << walk.s.keys) - 1;
+    int node0 = 0;       // the node of the first tail row
+    {
+      const TreeSeq seq = tree_seq<MT>(a, walk.b);
+      node0 = -seq.hot;
+      if (live && seq.keys > 0) {
+        nodes = a.mask ? a.mask[static_cast<size_t>(walk.b) * a.max_tree + t] : (~0ull >> (63 - t));
+        if (seq.keys < 64) nodes &= (1ull << seq.keys) - 1;
+      }
     }
-    const int cold_tiles = (walk.s.cold + kTK - 1) / kTK;
     float m = -INFINITY, l = 0.f, ref = 1.f;
     uint64_t odd = 0;    // attended nodes whose V is not finite
     for (int ti = walk.t0; ti < walk.t1; ti++, j++, mine++) {
       const int buf = MT == 1 ? mine & 1 : mt;
-      const uint32_t ph = MT == 1 ? (mine >> 1) & 1 : mine & 1;
       const uint32_t t_s = tmem + lanes + 128 * buf;
       // (a row tile that sat out a segment may have missed phases of mfull: S
       // first, whose phases are its own)
-      if (!tree_wait_warp(sm, &sm.sfull[buf], ph, a)) return;
-      if (!tree_wait_warp(sm, &sm.mfull[j % kTreeMeta], (j / kTreeMeta) & 1, a)) return;
+      if (!tree_wait_warp(sm, &sm.sfull[buf], (MT == 1 ? mine >> 1 : mine) & 1, a)) return;
+      if (!tree_wait_warp(sm, &sm.mfull[j & (kTreeMeta - 1)], (j / kTreeMeta) & 1, a)) return;
       tc_fence_after();
       if (warp_live) {
-        const TreeMeta &me = sm.meta[j % kTreeMeta];
-        uint32_t ok[4];
-#pragma unroll
-        for (int c = 0; c < 4; c++) ok[c] = me.ok[c];
-        if (ti >= cold_tiles) {
-          const int r0 = (ti - cold_tiles) * kTK - walk.s.hot;  // first row of the tile, as a node
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            const int k = r0 + 32 * c;  // node of the unit's first key
-            uint32_t own = 0;
-            if (k >= 0) own = k < 64 ? static_cast<uint32_t>(nodes >> k) : 0u;
-            else if (k > -32) own = static_cast<uint32_t>(nodes << -k);
-            ok[c] |= own;
-            uint32_t bad = 0;
-#pragma unroll
-            for (int w = 0; w < kTreeProducers; w++) bad |= me.bad[w][c];
-            bad &= own;
-            if (bad) odd |= k >= 0 ? static_cast<uint64_t>(bad) << k : static_cast<uint64_t>(bad) >> -k;
-          }
-        }
-        float ks[4], vs[4];
+        const TreeMeta &me = sm.meta[j & (kTreeMeta - 1)];
+        const bool tail = ti >= cold_tiles;
+        const int k0 = node0 + (ti - cold_tiles) * kTK;
+        bool plain = true;  // every key attended, no negative scale: the maximum of S times the scale
         float vmax = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; c++) {
-          ks[c] = me.k_scale[c] * a.qk_scale;
-          vs[c] = me.v_scale[c];
-          vmax = fmaxf(vmax, fabsf(vs[c]));
+          plain &= tree_ok(me, c, tail, k0 + 32 * c, nodes, odd) == 0xffffffffu && me.k_scale[c] * a.qk_scale >= 0.f;
+          vmax = fmaxf(vmax, fabsf(me.v_scale[c]));
         }
-        const bool full = __all_sync(0xffffffffu, (ok[0] & ok[1] & ok[2] & ok[3]) == 0xffffffffu);
-        // the tile's maximum
+        plain = __all_sync(0xffffffffu, plain);
         float top = -INFINITY;
-        uint32_t v[32];
-#pragma unroll
-        for (int c = 0; c < 4; c++) {
-          tc_ld32(t_s + 32 * c, v);
+        uint32_t v[64];
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {
+          tc_ld64(t_s + 64 * h, v);
           tc_wait_ld(v);
-          if (!full || ks[c] < 0.f) {
+          const float s0 = me.k_scale[2 * h] * a.qk_scale, s1 = me.k_scale[2 * h + 1] * a.qk_scale;
+          if (plain) {
+            top = fmaxf(top, fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1));
+          } else {
+            const uint32_t ok0 = tree_ok(me, 2 * h, tail, k0 + 64 * h, nodes, odd);
+            const uint32_t ok1 = tree_ok(me, 2 * h + 1, tail, k0 + 64 * h + 32, nodes, odd);
 #pragma unroll
             for (int k = 0; k < 32; k++) {
-              const float z = __uint_as_float(v[k]) * ks[c];
-              top = fmaxf(top, ok[c] >> k & 1 ? z : -INFINITY);
+              if (ok0 >> k & 1) top = fmaxf(top, __uint_as_float(v[k]) * s0);
+              if (ok1 >> k & 1) top = fmaxf(top, __uint_as_float(v[k + 32]) * s1);
             }
-          } else {
-            top = fmaxf(top, max32(v) * ks[c]);
           }
         }
         // m and r follow when they lag too far behind; O and l follow them
         const bool first = ti == walk.t0;
         float r_new = ref;
         if (first || vmax > kLagScale * ref) r_new = vmax > 0.f ? vmax : ref;
-        const bool move = first || top > m + kLagLog2;
-        const float m_new = move ? fmaxf(m, top) : m;
+        const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
         if (!first && __any_sync(0xffffffffu, m_new != m || r_new != ref)) {
           if (!tree_wait_warp(sm, &sm.odone[mt][(mine - 1) & 1], ((mine - 1) >> 1) & 1, a)) return;
           tc_fence_after();
           const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
           l *= f;
           const float g = f * __fdividef(ref, r_new);
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            tc_ld32(t_o + 32 * c, v);
+#pragma unroll 1
+          for (int h = 0; h < 2; h++) {
+            tc_ld64(t_o + 64 * h, v);
             tc_wait_ld(v);
 #pragma unroll
-            for (int k = 0; k < 32; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) * g);
-            tc_st32(t_o + 32 * c, v);
+            for (int k = 0; k < 64; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) * g);
+            tc_st64(t_o + 64 * h, v);
           }
         }
         m = m_new;
@@ -828,25 +827,33 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         const float base = m == -INFINITY ? 0.f : m;
         const float inv = __fdividef(1.f, ref);
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; c++) {
-          tc_ld32(t_s + 32 * c, v);
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {
+          tc_ld64(t_s + 64 * h, v);
           tc_wait_ld(v);
-          const float f = vs[c] * inv;
-          uint32_t p[16];
+          const float s0 = me.k_scale[2 * h] * a.qk_scale, s1 = me.k_scale[2 * h + 1] * a.qk_scale;
+          const float f0 = me.v_scale[2 * h] * inv, f1 = me.v_scale[2 * h + 1] * inv;
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float x = ex2(fmaf(__uint_as_float(v[k]), ks[c], -base));
-            float y = ex2(fmaf(__uint_as_float(v[k + 1]), ks[c], -base));
-            if (!full) {
-              x = ok[c] >> k & 1 ? x : 0.f;
-              y = ok[c] >> (k + 1) & 1 ? y : 0.f;
+          for (int k = 0; k < 64; k++)
+            v[k] = __float_as_uint(ex2(fmaf(__uint_as_float(v[k]), k < 32 ? s0 : s1, -base)));
+          if (!plain) {
+            const uint32_t ok0 = tree_ok(me, 2 * h, tail, k0 + 64 * h, nodes, odd);
+            const uint32_t ok1 = tree_ok(me, 2 * h + 1, tail, k0 + 64 * h + 32, nodes, odd);
+#pragma unroll
+            for (int k = 0; k < 32; k++) {
+              if (!(ok0 >> k & 1)) v[k] = 0;
+              if (!(ok1 >> k & 1)) v[k + 32] = 0;
             }
-            sum[(k >> 1) & 3] += x + y;
-            const __half2 h = __floats2half2_rn(x * f, y * f);
-            p[k >> 1] = *reinterpret_cast<const uint32_t *>(&h);
           }
-          tc_st16(t_s + 16 * c, p);
+          uint32_t p[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]), f = k < 32 ? f0 : f1;
+            sum[(k >> 1) & 3] += x + y;
+            const __half2 w = __floats2half2_rn(x * f, y * f);
+            p[k >> 1] = *reinterpret_cast<const uint32_t *>(&w);
+          }
+          tc_st32(t_s + 32 * h, p);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc_wait_st();
@@ -859,48 +866,47 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
     if (!tree_wait_warp(sm, &sm.odone[mt][(mine - 1) & 1], ((mine - 1) >> 1) & 1, a)) return;
     tc_fence_after();
     if (warp_live) {
-      const bool whole = walk.t0 == 0 && walk.t1 == walk.s.tiles;
+      const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
       const float o_scale = whole ? (l != 0.f ? ref / l : 0.f) : ref;
-      const int hq = walk.hk * G + row - t * G;
-      const size_t out_row = (static_cast<size_t>(walk.b) * a.max_tree + t) * a.hq + hq;
+      const size_t out_row = (static_cast<size_t>(walk.b) * a.max_tree + t) * a.hq + walk.hk * G + row - t * G;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (walk.t0 == 0 ? 1 : 0);
       const int pr = mt * 128 + row_in;
 #pragma unroll 1
-      for (int c = 0; c < 4; c++) {
-        uint32_t v[32];
-        tc_ld32(t_o + 32 * c, v);
+      for (int h = 0; h < 2; h++) {
+        uint32_t v[64];
+        tc_ld64(t_o + 64 * h, v);
         tc_wait_ld(v);
-        float o[32];
 #pragma unroll
-        for (int k = 0; k < 32; k++) o[k] = (l != 0.f ? __uint_as_float(v[k]) : 0.f) * o_scale;
-        if (odd) {
-          for (uint64_t rest = odd; rest; rest &= rest - 1) {
-            const int node = __ffsll(static_cast<long long>(rest)) - 1;
-            const __half *vr = a.v_tree + ((static_cast<size_t>(walk.b) * a.max_tree + node) * a.hkv + walk.hk) * kDim;
+        for (int k = 0; k < 64; k++) v[k] = __float_as_uint((l != 0.f ? __uint_as_float(v[k]) : 0.f) * o_scale);
+        for (uint64_t rest = odd; rest; rest &= rest - 1) {
+          const int node = __ffsll(static_cast<long long>(rest)) - 1;
+          const __half *vr =
+              a.v_tree + ((static_cast<size_t>(walk.b) * a.max_tree + node) * a.hkv + walk.hk) * kDim + 64 * h;
 #pragma unroll
-            for (int k = 0; k < 32; k++) {
-              const __half h = vr[32 * c + k];
-              if (f16_not_finite(__half_as_ushort(h))) o[k] += __half2float(h);
-            }
+          for (int k = 0; k < 64; k += 2) {
+            const __half2 x = *reinterpret_cast<const __half2 *>(vr + k);
+            if (f16_not_finite(__half_as_ushort(x.x))) v[k] = __float_as_uint(__uint_as_float(v[k]) + __low2float(x));
+            if (f16_not_finite(__half_as_ushort(x.y)))
+              v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + __high2float(x));
           }
         }
         if (!live) continue;
         if (whole) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t h[4];
+          for (int k = 0; k < 64; k += 8) {
+            uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-              const __half2 x = __floats2half2_rn(o[k + 2 * e], o[k + 2 * e + 1]);
-              h[e] = *reinterpret_cast<const uint32_t *>(&x);
+              const __half2 x = __floats2half2_rn(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1]));
+              w[e] = *reinterpret_cast<const uint32_t *>(&x);
             }
-            *reinterpret_cast<uint4 *>(a.out + out_row * kDim + 32 * c + k) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(a.out + out_row * kDim + 64 * h + k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(a.part_o) + slot * 32 * 128 * MT;
+          uint4 *dst = reinterpret_cast<uint4 *>(a.part_o) + slot * 32 * 128 * MT;
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            dst[(8 * c + (k >> 2)) * (128 * MT) + pr] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 64; k += 4)
+            dst[(16 * h + (k >> 2)) * (128 * MT) + pr] = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
       }
       if (live) {
@@ -918,8 +924,10 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
     // who has the unit's tiles, from the CTA with its first
     if (threadIdx.x == 0 && walk.t0 == 0) {
       const long long ctas = min(static_cast<long long>(a.ctas), sm.total);
-      const long long u0 = walk.w - walk.t1;  // the list's index of the unit's first tile
-      const int last = static_cast<int>(((u0 + walk.s.tiles) * ctas - 1) / sm.total);
+      // the list's index of the unit's last tile, and the run that has it
+      const long long end = sm.total * blockIdx.x / ctas + j - (walk.t1 - walk.t0) + walk.tiles;
+      const int last = static_cast<int>((end * ctas - 1) / sm.total);
+      const int groups_max = (a.max_tree * G + 128 * MT - 1) / (128 * MT);
       a.unit_ctas[(static_cast<size_t>(walk.b) * a.hkv + walk.hk) * groups_max + walk.mg] =
           make_int2(static_cast<int>(blockIdx.x), last);
     }
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(TreeShape<MT>::kThreads, 1) tree_kernel(const 
                                                        2 * kTreeStages * kTreeOperand);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
-  constexpr int kMmaWarp = Shape::kSoftWarps + kTreeProducers;
+  constexpr int kMmaWarp = Shape::kSoftWarps + Shape::kProducers;
 
   // the list's length and where this CTA's run starts: every thread sums a
   // range of sequences, a scan over the threads places them
@@ -945,7 +953,7 @@ __global__ void __launch_bounds__(TreeShape<MT>::kThreads, 1) tree_kernel(const 
   long long mine = 0;
   for (int b = b0; b < b1; b++) {
     const TreeSeq s = tree_seq<MT>(a, b);
-    mine += s.span;
+    mine += static_cast<long long>(s.tiles) * s.groups * a.hkv;
     if (blockIdx.x == 0 && s.status) set_status(a.status, s.status);
   }
   long long inc = mine;
@@ -958,14 +966,14 @@ __global__ void __launch_bounds__(TreeShape<MT>::kThreads, 1) tree_kernel(const 
   if (tid == 0) {
     sm.abort = 0;
     for (int i = 0; i < kTreeStages; i++) {
-      mbar_init(&sm.kfull[i], kTreeProducers);
+      mbar_init(&sm.kfull[i], Shape::kProducers);
       mbar_init(&sm.kempty[i], 1);
-      mbar_init(&sm.vfull[i], kTreeProducers);
+      mbar_init(&sm.vfull[i], Shape::kProducers);
       mbar_init(&sm.vempty[i], 1);
     }
-    for (int i = 0; i < kTreeMeta; i++) mbar_init(&sm.mfull[i], kTreeProducers);
+    for (int i = 0; i < kTreeMeta; i++) mbar_init(&sm.mfull[i], Shape::kProducers);
     for (int i = 0; i < TreeSmem<MT>::kQ; i++) {
-      mbar_init(&sm.qfull[i], kTreeProducers);
+      mbar_init(&sm.qfull[i], Shape::kProducers);
       mbar_init(&sm.qempty[i], 1);
     }
     for (int i = 0; i < 2; i++) {
@@ -988,14 +996,16 @@ __global__ void __launch_bounds__(TreeShape<MT>::kThreads, 1) tree_kernel(const 
   }
   const long long ctas = min(static_cast<long long>(gridDim.x), total);
   if (static_cast<long long>(blockIdx.x) >= ctas) return;  // the whole CTA: nothing to do
-  const long long w0 = total * blockIdx.x / ctas, w1 = total * (blockIdx.x + 1) / ctas;
+  const long long w0 = total * blockIdx.x / ctas;
+  const int n_tiles = static_cast<int>(total * (blockIdx.x + 1) / ctas - w0);
   long long at = before + inc - mine;
   if (w0 >= at && w0 < at + mine) {
     for (int b = b0; b < b1; b++) {
-      const long long span = tree_seq<MT>(a, b).span;
+      const TreeSeq s = tree_seq<MT>(a, b);
+      const long long span = static_cast<long long>(s.tiles) * s.groups * a.hkv;
       if (w0 < at + span) {
         sm.start_b = b;
-        sm.start_base = at;
+        sm.start_pos = w0 - at;
         sm.total = total;
         break;
       }
@@ -1009,12 +1019,12 @@ __global__ void __launch_bounds__(TreeShape<MT>::kThreads, 1) tree_kernel(const 
   const uint32_t tmem = sm.tmem;
 
   if (warp < Shape::kSoftWarps) {
-    tree_softmax<MT>(a, sm, tmem, w0, w1);
+    tree_softmax<MT>(a, sm, tmem, n_tiles);
   } else if (warp < kMmaWarp) {
-    tree_produce<MT, kF16>(a, sm, q_s, k_s, v_s, w0, w1);
+    tree_produce<MT, kF16>(a, sm, q_s, k_s, v_s, n_tiles);
   } else {
     if (lane == 0) {
-      tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, w0, w1);
+      tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles);
       // no MMA is in flight when TMEM is given back
       tc_commit(&sm.drain);
       if (!mbar_wait_bounded(&sm.drain, 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);

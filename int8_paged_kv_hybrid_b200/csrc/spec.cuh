@@ -29,15 +29,17 @@ struct TreeArgs {
   int lsub;                   // log2 of the 64-token sub-blocks per block
   int bshift;                 // log2 of the tokens per block
   float qk_scale;             // softmax_scale * log2(e)
+  int group;                  // Hq / Hkv
+  int group_recip;            // 2^16 / group, rounded up
   uint32_t wait_cycles;       // limit (SM cycles) of the bounded waits
   int ctas;                   // CTAs of the launch
-  int wide;                   // cold pool 32-byte aligned: 32-byte loads
-  // partial results of units that several CTAs share (see tree.cu): sums and
-  // maxima [2 ctas][rows], outputs [2 ctas][32][rows][4], rows = 128 * MT, and
-  // the CTAs {first, last} of every unit [batch][Hkv][groups]
+  // units that several CTAs share (see tree.cu): sums and maxima [2 ctas][rows]
+  // and outputs [2 ctas][32][rows][4] of the CTAs' parts, rows = 128 * MT, and for
+  // each CTA the unit it has the first tile of {sequence, kv head, row group,
+  // later CTAs} (0 later CTAs: none)
   float *part_ml;
   float *part_o;
-  int2 *unit_ctas;
+  int4 *shared_units;
 };
 
 struct PoolArgs {

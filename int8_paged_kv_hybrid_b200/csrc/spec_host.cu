@@ -37,7 +37,7 @@ int check_geometry(const hyb_pool_desc *p) {
 extern "C" {
 
 // Workspace of hyb_tree_attn: the partial outputs, their sums and maxima, and
-// the CTAs of every unit (TreeArgs), each part on a 256-byte boundary.
+// the units that CTAs share (TreeArgs).
 struct TreeWs {
   size_t o, ml, units, total;
 };
@@ -49,8 +49,7 @@ static TreeWs tree_ws(const hyb_cache_desc *d, int32_t max_tree, int sms) {
   w.o = 0;
   w.ml = w.o + rows * hyb::kDim * sizeof(float);
   w.units = w.ml + rows * 2 * sizeof(float);
-  const size_t units = static_cast<size_t>(d->batch) * d->num_kv_heads * hyb::tree_groups(max_tree, group);
-  w.total = w.units + units * sizeof(int2);
+  w.total = w.units + static_cast<size_t>(sms) * sizeof(int4);
   return w;
 }
 
@@ -77,10 +76,11 @@ int hyb_tree_attn(const hyb_cache_desc *d, const void *q, const void *k_tree, co
   const long long wait = hyb::host_wait_cycles();
   a.wait_cycles = wait < 0xf0000000ll ? static_cast<uint32_t>(wait) : 0xf0000000u;
   a.ctas = sms;
-  a.wide = aligned(d->cold, 32);
+  a.group = d->num_q_heads / d->num_kv_heads;
+  a.group_recip = 65536 / a.group + 1;
   a.part_o = reinterpret_cast<float *>(ws + w.o);
   a.part_ml = reinterpret_cast<float *>(ws + w.ml);
-  a.unit_ctas = reinterpret_cast<int2 *>(ws + w.units);
+  a.shared_units = reinterpret_cast<int4 *>(ws + w.units);
   a.hot = static_cast<const uint8_t *>(d->hot);
   a.cold = static_cast<const uint8_t *>(d->cold);
   a.scales = d->scales;

@@ -22,16 +22,16 @@
 // inside one run is finished there; the others leave (O, m, l) per CTA, and
 // tree_combine_kernel merges them in the order of the tiles.
 //
-// Inside a CTA (18 warps): a scout warp looks the tiles up (block table, scales,
-// segment ends) some tiles ahead, writes their records and starts their way
-// into L2; two groups of four producer warps take turns at the tiles and bring
-// codes or rows to FP16 in the 128-byte swizzled layout of the
-// MMA's shared operands; one thread issues the MMAs; two groups of four softmax
-// warps (one query row per thread) keep two softmax streams and write the
-// weights back over the logits in TMEM, where the second product reads them as
-// its A operand.  The streams are the two row tiles (MT 2), or the even and the
-// odd tiles of the run (MT 1), which are merged at a unit's end: either way a
-// stream's softmax has the time of two tiles' MMAs.
+// Inside a CTA (19 warps): a scout warp looks the tiles up (block table, scales,
+// segment ends) some tiles ahead, writes their records, starts their way into
+// L2 and fetches the query rows; two groups of four producer warps take turns
+// at the tiles and bring codes or rows to FP16 in the 128-byte swizzled layout
+// of the MMA's shared operands; two groups of four softmax warps (one query row
+// per thread) keep two softmax streams and write the weights over the logits in
+// TMEM, where the second product reads them as its A operand; a warp for each
+// stream issues its MMAs.  The streams are the two row tiles (MT 2), or the
+// even and the odd tiles of the run (MT 1), merged at a unit's end; then
+// everything from the stage in shared memory on is one stream's own.
 #include "kernels.cuh"
 #include "spec.cuh"
 #include "tc05.cuh"
@@ -47,18 +47,17 @@ constexpr uint32_t kTreeSlab = kTreeOperand / 2;  // its halves of 64 columns
 constexpr float kLagLog2 = 6.f;
 constexpr float kLagScale = 256.f;
 
-// Warps: softmax, producers, MMA, scout.  A launch gives every thread 96
-// registers (65536 / 20 warps); the producers, which hold a tile's codes, take 8
-// of each softmax thread's.
-constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeGroups = 2;
-constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + 2);
-constexpr int kTreeSoftRegs = 88, kTreeProdRegs = 104;
+// Warps: softmax, producers, MMA, scout (20 warps of 96 registers fill an SM).
+constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeGroups = 2, kTreeMma = 2;
+constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + kTreeMma + 1);
 
-// TreeRec::flags: the first, the second and the last tile of its segment; every
-// key attended by every row and no negative scale; cold (not ring and nodes);
-// the unit's row tiles; the segment's number modulo 4
-constexpr uint32_t kTileFirst = 1, kTileSecond = 2, kTileLast = 4, kTilePlain = 8, kTileCold = 16;
-constexpr int kTileRowsShift = 5, kTileSegShift = 7;
+// TreeRec::flags: the first, the second and the last tile of its segment (the
+// part of a unit that this CTA has); every key attended by every row and no
+// negative scale; cold (not ring and nodes); the segment has the unit's first,
+// its last tile; the segment's number modulo 4
+constexpr uint32_t kTileFirst = 1, kTileSecond = 2, kTileLast = 4, kTilePlain = 8, kTileCold = 16, kUnitStart = 32,
+                   kUnitEnd = 64;
+constexpr int kTileSegShift = 7;
 
 // A tile of 128 keys in four units of 32, as the scout found it.
 struct TreeRec {
@@ -70,9 +69,14 @@ struct TreeRec {
   uint32_t fmt;          // bit c: unit c is INT4; bit 4 + c: it is the second half of its slots
   uint32_t flags;
   float v_max;           // largest |v_scale|
+  int left;              // tiles of the segment after this one
+  int rest;              // tiles of the unit after this one
   int b, hk, mg;         // the unit's sequence, kv head and row group
-  int cold, hot, keys;   // tail: cold and ring tokens, nodes
-  int row0;              // tail: its first row (ring rows, then nodes)
+  int rows;              // query rows of the sequence and kv head
+  // tail: its first row (ring rows in the order of their positions, then
+  // nodes), the cold and ring tokens and the nodes; the ring and the nodes' K, V
+  int row0, cold, hot, keys;
+  const __half *ring, *node[2];
 };
 
 // A stream's row at a segment's end (MT 1).
@@ -84,21 +88,22 @@ struct TreeStat {
 template <int MT>
 struct TreeSmem {
   static constexpr int kQ = MT == 1 ? 2 : 1;  // Q buffers
+  // MMA operands: MT 1 stage and stream are one; MT 2 both streams free a stage
   uint64_t kfull[kTreeStages], kempty[kTreeStages], vfull[kTreeStages], vempty[kTreeStages];
-  uint64_t rfull[2], rfree[2];  // records, by batch parity
-  uint64_t mfull[kTreeRecs];    // a record's tile is in shared memory
-  uint64_t qfull[kQ], qempty[kQ];
-  uint64_t sfull[2], pfull[2], odone[2];  // by stream
-  uint64_t ofree[2];                      // by stream (MT 1: one for both)
-  uint64_t xfull;                         // MT 1: the streams' rows are in `stat`
-  uint64_t drain;
+  uint64_t rfull[2], rfree[2];     // records, by batch parity
+  uint64_t mfull[kTreeRecs];       // a record's tile is in shared memory
+  uint64_t qfull[kQ];
+  uint64_t qempty[kQ][2];          // by stream
+  uint64_t sfull[2], pfull[2], odone[2], ofree[2];  // by stream
+  uint64_t xfull;                  // MT 1: both streams' rows are in `stat`
+  uint64_t drain[2];
   TreeRec rec[kTreeRecs];
   uint32_t tmem;
   volatile int abort;
   int start_b;
-  long long start_pos, total;  // the run's start within sequence start_b, the list's length
+  long long start_pos, total;      // the run's start within sequence start_b; the list's length
   long long warp_sum[32];
-  TreeStat stat[MT == 1 ? 2 : 1][MT == 1 ? 2 : 1][MT == 1 ? 128 : 1];  // [segment parity][stream][row]
+  TreeStat stat[MT == 1 ? 2 : 1][MT == 1 ? 2 : 1][MT == 1 ? 128 : 1];  // [parity][stream][row]
 };
 
 template <int MT>
@@ -131,69 +136,39 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   s.hot = bad ? 0 : L - s.cold;
   s.keys = bad ? 0 : s.nt;
   s.tiles = max(1, (s.cold + kTK - 1) / kTK + (s.hot + s.keys + kTK - 1) / kTK);
-  s.groups = (s.nt * (a.hq / a.hkv) + 128 * MT - 1) / (128 * MT);
+  s.groups = (s.nt * a.group + 128 * MT - 1) / (128 * MT);
   return s;
 }
 
-// A run of `left` tiles from tile `pos` of sequence b on, taken unit by unit.
-template <int MT>
-struct TreeWalk {
-  long long pos;
-  int left, b;
-  int cold, tiles, groups, nt;
-  int hk, mg, t0, t1;  // the current segment: tiles [t0, t1) of unit (b, hk, mg)
-
-  __device__ __forceinline__ void enter(const TreeArgs &a) {
-    const TreeSeq s = tree_seq<MT>(a, b);
-    cold = s.cold;
-    tiles = s.tiles;
-    groups = s.groups;
-    nt = s.nt;
-  }
-  __device__ __forceinline__ bool next(const TreeArgs &a) {
-    if (left == 0) return false;
-    for (;;) {
-      const long long span = static_cast<long long>(tiles) * groups * a.hkv;
-      if (pos < span) break;
-      pos -= span;
-      b++;
-      enter(a);
-    }
-    const int unit = static_cast<int>(pos / tiles);
-    t0 = static_cast<int>(pos - static_cast<long long>(unit) * tiles);
-    t1 = min(tiles, t0 + left);
-    hk = unit / groups;
-    mg = unit - hk * groups;
-    pos += t1 - t0;
-    left -= t1 - t0;
-    return true;
-  }
-  // 128-row tiles of this unit that have a row
-  __device__ __forceinline__ int m_tiles(const TreeArgs &a) const {
-    return MT == 1 ? 1 : min(MT, (nt * (a.hq / a.hkv) - mg * 128 * MT + 127) / 128);
-  }
-};
-
-// Wait for phase `parity`; false when the wait or the kernel gave up.
+// Wait for phase `parity`; false (in all lanes) when the wait or the kernel
+// gave up.  Called by whole warps.
 template <typename Sm>
 __device__ __forceinline__ bool tree_wait(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
   const bool quick = a.wait_cycles < kShortWaitCycles;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
-  while (!(quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
-    if (sm.abort) return false;
-    if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
-      sm.abort = 1;
-      set_status(a.status, HYB_STATUS_TIMEOUT);
-      return false;
+  bool ok = quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+    while (!ok) {
+      ok = quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+      if (ok || sm.abort) break;
+      if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
+        sm.abort = 1;
+        set_status(a.status, HYB_STATUS_TIMEOUT);
+        break;
+      }
     }
+    ok = __all_sync(0xffffffffu, ok);
   }
-  return true;
+  return ok;
 }
 
-// The same for all lanes of a warp, with one answer.
-template <typename Sm>
-__device__ __forceinline__ bool tree_wait_warp(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  return __all_sync(0xffffffffu, tree_wait(sm, bar, parity, a));
+// The node of a query row: row / (Hq / Hkv), by a multiplication that is exact
+// for rows below 2^13 (there are at most 64 * 8).
+__device__ __forceinline__ int row_node(const TreeArgs &a, int row) { return (row * a.group_recip) >> 16; }
+
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -208,37 +183,38 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 
 // ---- producers ----
 
-// Eight codes (two words of four bytes, biased by 2^(bits-1)) as FP16: byte u
-// under the exponent of 1024 is 1024 + u, and the subtraction is exact.
-__device__ __forceinline__ uint4 f16_codes(uint32_t lo, uint32_t hi, uint32_t bias) {
-  const __half2 off = __halves2half2(__ushort_as_half(static_cast<unsigned short>(bias)),
-                                     __ushort_as_half(static_cast<unsigned short>(bias)));
-  auto two = [&](uint32_t x, uint32_t sel) {
+// Codes as FP16: a byte u = code + 2^(bits-1) under the exponent of 1024 is 1024
+// + u, and the subtraction of 1024 + 2^(bits-1) is exact.  `flip` takes a code's
+// byte to u.
+struct TreeCodec {
+  uint32_t flip, off;
+  __device__ __forceinline__ explicit TreeCodec(bool int4)
+      : flip(int4 ? 0x08080808u : 0x80808080u), off(int4 ? 0x64086408u : 0x64806480u) {}
+  __device__ __forceinline__ uint32_t two(uint32_t x, uint32_t sel) const {
     const uint32_t h = __byte_perm(x, 0x64646464u, sel);
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), off);
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&off));
     return *reinterpret_cast<const uint32_t *>(&d);
-  };
-  return make_uint4(two(lo, 0x4140), two(lo, 0x4342), two(hi, 0x4140), two(hi, 0x4342));
-}
-__device__ __forceinline__ uint4 f16_int8(uint32_t w0, uint32_t w1) {  // eight INT8 codes
-  return f16_codes(w0 ^ 0x80808080u, w1 ^ 0x80808080u, 0x6480);        // 1024 + 128
-}
-__device__ __forceinline__ uint4 f16_int4(uint32_t w) {  // eight INT4 codes of a word
-  return f16_codes((w & 0x0f0f0f0fu) ^ 0x08080808u, ((w >> 4) & 0x0f0f0f0fu) ^ 0x08080808u, 0x6408);  // 1024 + 8
+  }
+  __device__ __forceinline__ uint4 eight(uint32_t w0, uint32_t w1) const {
+    w0 ^= flip;
+    w1 ^= flip;
+    return make_uint4(two(w0, 0x4140), two(w0, 0x4342), two(w1, 0x4140), two(w1, 0x4342));
+  }
+};
+
+// Sixteen bytes of INT4 codes (r[0]) become 32 bytes, a code in the low half of
+// each: code e of a word is the low nibble of byte e, e + 4 the high nibble.
+// `swap`: the second eight bytes come first.
+__device__ __forceinline__ void widen4(uint4 *r, bool swap) {
+  const uint4 x = swap ? make_uint4(r[0].z, r[0].w, r[0].x, r[0].y) : r[0];
+  const uint32_t m = 0x0f0f0f0fu;
+  r[0] = make_uint4(x.x & m, x.x >> 4 & m, x.y & m, x.y >> 4 & m);
+  r[1] = make_uint4(x.z & m, x.z >> 4 & m, x.w & m, x.w >> 4 & m);
 }
 
 __device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
-// A thread of a producer group has a part of each of a tile's four units of 32
-// keys: K of key tid / 4, 32 channels; V of INT8 / INT4 channel tid, all 32
-// keys, of FP16 rows channels 2 (tid % 64), + 1 and 16 keys.
-
-// [p, p + bytes) on its way into L2; 16-byte aligned.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-// Codes are read once: no place in L1.
+// Codes and rows are read once: no place in L1.
 __device__ __forceinline__ uint4 ldg16(const void *p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -246,92 +222,86 @@ __device__ __forceinline__ uint4 ldg16(const void *p) {
                : "l"(p));
   return r;
 }
-__device__ __forceinline__ void ldg32(const void *p, uint4 &x, uint4 &y) {  // 32-byte aligned
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-               : "l"(p));
-}
 
-// Codes of a unit: the thread's 32 bytes (INT4: 16) of K or V of the 64-token
-// tile pair at `pair` that holds the unit as slots 32 half ...
-__device__ __forceinline__ void load_codes(const TreeArgs &a, const uint8_t *p, uint4 (&r)[2]) {
-  if (a.wide) {
-    ldg32(p, r[0], r[1]);
-  } else {
-    r[0] = ldg16(p);
-    r[1] = ldg16(p + 16);
-  }
-}
+// A thread of a producer group has a part of each of a tile's four units of 32
+// keys.  K: key tid / 4, channels 32 (tid % 4) and up.  Eight lanes are two
+// keys of four threads; threads 2 and 3 of a key take their chunks in the order
+// j ^ 2, which spreads the eight over the banks.
+struct TreeK {
+  uint32_t row, chan;  // key of the unit, first channel
+  uint32_t at[4];      // unit 0's place of chunk j (the j-th that the thread holds)
+  uint32_t swap;       // 0 or 2: the first chunk held
 
-__device__ __forceinline__ void load_k(const TreeArgs &a, const uint8_t *pair, int half, bool int4, int tid, uint4 (&k)[2]) {
-  const int slot = 32 * half + (tid >> 2);
-  if (int4) k[0] = ldg16(pair + slot * 64 + 16 * (tid & 3));
-  else load_codes(a, pair + slot * 128 + 32 * (tid & 3), k);
-}
-
-// (V: the unit's two 16-slot chunks are one aligned pair, swapped where the
-// swizzle's lowest bit is set; store_v8 puts them right)
-__device__ __forceinline__ void load_v(const TreeArgs &a, const uint8_t *pair, int half, bool int4, int tid, uint4 (&v)[2]) {
-  const uint8_t *t = pair + kTileBytes;
-  if (int4) v[0] = ldg16(t + tid * 32 + 8 * ((2 * half) ^ ((tid >> 2) & 2)));
-  else load_codes(a, t + tid * 64 + 16 * ((2 * half) ^ ((tid >> 1) & 2)), v);
-}
-
-// K of one unit into the operand: row = key, 32 channels = four 16-byte chunks
-// of a 64-channel slab.  Eight lanes are two rows of four threads; threads 2
-// and 3 of a row write their chunks in the order k ^ 2, which spreads the
-// eight over the banks.
-__device__ __forceinline__ void store_k16(uint32_t st, int u, int tid, const uint4 (&k)[4]) {
-  const int row = 32 * u + (tid >> 2), i = tid & 3;
-  const uint32_t base = st + (i >> 1) * kTreeSlab + row * 128;
+  __device__ __forceinline__ TreeK(uint32_t st, int tid) {
+    row = tid >> 2;
+    chan = 32 * (tid & 3);
+    swap = tid & 2;
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const uint4 x = i & 2 ? k[j ^ 2] : k[j];
-    const int c = 4 * (i & 1) + (i & 2 ? j ^ 2 : j);
-    sts128(base + ((c ^ (row & 7)) << 4), x);
+    for (int j = 0; j < 4; j++)
+      at[j] = st + ((tid >> 1) & 1) * kTreeSlab + row * 128 + (((4 * (tid & 1) + (j ^ swap)) ^ (row & 7)) << 4);
   }
-}
+  __device__ __forceinline__ void load(const uint8_t *pair, int half, bool int4, uint4 *r) const {
+    if (int4) {
+      r[0] = ldg16(pair + (32 * half + row) * 64 + chan / 2);
+      r[1] = make_uint4(0, 0, 0, 0);
+    } else {
+      const uint8_t *p = pair + (32 * half + row) * 128 + chan;
+      r[0] = ldg16(p + 8 * swap);
+      r[1] = ldg16(p + 16 - 8 * swap);
+    }
+  }
+  __device__ __forceinline__ void store(int u, bool int4, uint4 *r) const {
+    if (int4) widen4(r, swap);
+    const TreeCodec f(int4);
+    sts128(at[0] + 4096 * u, f.eight(r[0].x, r[0].y));
+    sts128(at[1] + 4096 * u, f.eight(r[0].z, r[0].w));
+    sts128(at[2] + 4096 * u, f.eight(r[1].x, r[1].y));
+    sts128(at[3] + 4096 * u, f.eight(r[1].z, r[1].w));
+  }
+  __device__ __forceinline__ void load_row(const __half *k, uint4 *r) const {
+#pragma unroll
+    for (int j = 0; j < 4; j++) r[j] = ldg16(k + chan + 8 * (j ^ swap));
+  }
+  __device__ __forceinline__ void store_row(int u, const uint4 *r) const {
+#pragma unroll
+    for (int j = 0; j < 4; j++) sts128(at[j] + 4096 * u, r[j]);
+  }
+};
 
-__device__ __forceinline__ void store_k8(uint32_t st, int u, int tid, bool int4, const uint4 (&k)[2]) {
-  uint4 f[4];
-  if (int4) {
-    f[0] = f16_int4(k[0].x);
-    f[1] = f16_int4(k[0].y);
-    f[2] = f16_int4(k[0].z);
-    f[3] = f16_int4(k[0].w);
-  } else {
-    f[0] = f16_int8(k[0].x, k[0].y);
-    f[1] = f16_int8(k[0].z, k[0].w);
-    f[2] = f16_int8(k[1].x, k[1].y);
-    f[3] = f16_int8(k[1].z, k[1].w);
-  }
-  store_k16(st, u, tid, f);
-}
+// V of INT8 / INT4 units: channel tid, all 32 keys of the unit.  Its two
+// 16-slot chunks are one aligned pair, swapped where the swizzle's lowest bit
+// is set: the halves are loaded in the order of the slots.  Eight lanes are
+// eight rows, all banks.
+struct TreeV {
+  uint32_t chan;
+  uint32_t at[4];  // unit 0's place of chunk j; odd units: ^ 64
 
-// V of one unit: row = channel, the unit's 32 keys = four chunks of a 64-key
-// slab; eight lanes are eight rows, all banks.
-__device__ __forceinline__ void store_v8(uint32_t st, int u, int tid, bool int4, const uint4 (&v)[2]) {
-  const int row = tid;
-  const uint32_t base = st + (u >> 1) * kTreeSlab + row * 128;
-  const int c = 4 * (u & 1);
-  if (int4) {
-    // the swap, as a bit of the chunk
-    const int x = (row & 7) ^ ((row >> 2 & 1) << 1);
-    sts128(base + (((c + 0) ^ x) << 4), f16_int4(v[0].x));
-    sts128(base + (((c + 1) ^ x) << 4), f16_int4(v[0].y));
-    sts128(base + (((c + 2) ^ x) << 4), f16_int4(v[0].z));
-    sts128(base + (((c + 3) ^ x) << 4), f16_int4(v[0].w));
-  } else {
-    // (here that would leave eight rows four places: the words swap)
-    const int x = row & 7;
-    const bool swap = row & 2;
-    const uint4 y = swap ? v[1] : v[0], z = swap ? v[0] : v[1];
-    sts128(base + (((c + 0) ^ x) << 4), f16_int8(y.x, y.y));
-    sts128(base + (((c + 1) ^ x) << 4), f16_int8(y.z, y.w));
-    sts128(base + (((c + 2) ^ x) << 4), f16_int8(z.x, z.y));
-    sts128(base + (((c + 3) ^ x) << 4), f16_int8(z.z, z.w));
+  __device__ __forceinline__ TreeV(uint32_t st, int tid) {
+    chan = tid;
+#pragma unroll
+    for (int j = 0; j < 4; j++) at[j] = st + chan * 128 + ((j ^ (chan & 7)) << 4);
   }
-}
+  __device__ __forceinline__ void load(const uint8_t *pair, int half, bool int4, uint4 *r) const {
+    if (int4) {
+      r[0] = ldg16(pair + kTileBytes + chan * 32 + 8 * ((2 * half) ^ ((chan >> 2) & 2)));
+      r[1] = make_uint4(0, 0, 0, 0);
+    } else {
+      const uint32_t x = (chan >> 1) & 3;
+      const uint8_t *p = pair + kTileBytes + chan * 64 + 16 * ((2 * half) ^ (x & 2));
+      r[0] = ldg16(p + 16 * (x & 1));
+      r[1] = ldg16(p + 16 - 16 * (x & 1));
+    }
+  }
+  __device__ __forceinline__ void store(int u, bool int4, uint4 *r) const {
+    if (int4) widen4(r, chan >> 2 & 1);
+    const TreeCodec f(int4);
+    const uint32_t odd = 64 * (u & 1), slab = (u >> 1) * kTreeSlab;
+    sts128((at[0] ^ odd) + slab, f.eight(r[0].x, r[0].y));
+    sts128((at[1] ^ odd) + slab, f.eight(r[0].z, r[0].w));
+    sts128((at[2] ^ odd) + slab, f.eight(r[1].x, r[1].y));
+    sts128((at[3] ^ odd) + slab, f.eight(r[1].z, r[1].w));
+  }
+};
 
 // FP16 V of one unit: the thread's two channels are two rows, its 16 keys two
 // chunks of each.  Lanes 4..7 of eight write their odd row first, so that the
@@ -354,177 +324,166 @@ __device__ __forceinline__ void store_v16(uint32_t st, int u, int tid, const uin
   }
 }
 
-// FP16 rows as units: the rows of an FP16 cold block, or of the tail (the
-// ring's in the order of their positions, then the nodes).
-struct TreeRows {
-  const TreeRec *rec;
-  const __half *base;  // cold rows; null: the tail
-  int n, r0;           // valid cold rows; the unit's first tail row
-
-  __device__ __forceinline__ TreeRows(const TreeRec &r, int c) : rec(&r) {
-    const bool cold = r.flags & kTileCold;
-    base = cold ? reinterpret_cast<const __half *>(r.at[c]) : nullptr;
-    n = cold ? __popc(r.ok[c]) : -1;
-    r0 = r.row0 + 32 * c;
-  }
-  // the K row (kv 1: V row) of key k of the unit, or null
-  __device__ __forceinline__ const __half *row(const TreeArgs &a, int k, int kv) const {
-    if (n >= 0) return k < n ? base + (2 * k + kv) * kDim : nullptr;
-    int r = r0 + k;
-    if (r < rec->hot)
-      return reinterpret_cast<const __half *>(a.hot) + (((static_cast<size_t>(rec->b) * a.hkv + rec->hk) * a.hot_tokens +
-                                                         ((rec->cold + r) & (a.hot_tokens - 1))) * 2 + kv) * kDim;
-    r -= rec->hot;
-    if (r >= rec->keys) return nullptr;
-    return (kv ? a.v_tree : a.k_tree) + ((static_cast<size_t>(rec->b) * a.max_tree + r) * a.hkv + rec->hk) * kDim;
-  }
-};
-
-__device__ __forceinline__ void rows_k(const TreeArgs &a, const TreeRows &x, int tid, uint4 (&k)[4]) {
-  const __half *row = x.row(a, tid >> 2, 0);
-#pragma unroll
-  for (int j = 0; j < 4; j++) k[j] = row ? ldg16(row + 32 * (tid & 3) + 8 * j) : make_uint4(0, 0, 0, 0);
-}
-
-__device__ __forceinline__ void rows_v(const TreeArgs &a, const TreeRows &x, int tid, uint32_t (&w)[16]) {
-  const int k0 = 16 * (tid >> 6), c = 2 * (tid & 63);
-#pragma unroll
-  for (int j = 0; j < 16; j++) {
-    const __half *r = x.row(a, k0 + j, 1);
-    w[j] = r ? __ldg(reinterpret_cast<const uint32_t *>(r + c)) : 0u;
-  }
-}
-
-// The query rows of a unit into its Q operand(s); rows beyond the tree are 0.
-template <int MT>
-__device__ __forceinline__ void load_q(const TreeArgs &a, const TreeRec &x, uint32_t st, int tid) {
-  const int G = a.hq / a.hkv, mg = x.mg;
-  const int rows = (a.n_tree ? a.n_tree[x.b] : a.max_tree) * G;
-#pragma unroll 4
-  for (int i = tid; i < 128 * MT * 16; i += 128) {
-    const int r = i >> 4, c = i & 15, row = mg * 128 * MT + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int t = row / G;
-      v = ldg16(a.q + ((static_cast<size_t>(x.b) * a.max_tree + t) * a.hq + x.hk * G + row - t * G) * kDim + 8 * c);
-    }
-    sts128(st + (r >> 7) * kTreeOperand + (c >> 3) * kTreeSlab + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4), v);
-  }
-}
-
-// (The MMA thread orders these writes before its MMAs with one proxy fence: a
-// fence here would wait for the thread's loads in flight.)
-__device__ __forceinline__ void producer_arrive(uint64_t *bar, int lane) {
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
+// The K row (kv 1: V row) of key k of unit c of a tile of FP16 rows, or null.
+__device__ __forceinline__ const __half *tree_row(const TreeArgs &a, const TreeRec &r, int c, int k, int kv) {
+  if (r.flags & kTileCold)
+    return r.ok[c] >> k & 1 ? reinterpret_cast<const __half *>(r.at[c]) + (2 * k + kv) * kDim : nullptr;
+  const int i = r.row0 + 32 * c + k;
+  if (i < r.hot) return r.ring + (2 * ((r.cold + i) & (a.hot_tokens - 1)) + kv) * kDim;
+  return i - r.hot < r.keys ? r.node[kv] + static_cast<size_t>(i - r.hot) * a.hkv * kDim : nullptr;
 }
 
 template <int MT, bool kF16>
-__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s,
-                                             uint32_t v_s, int n) {
+__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t k_s, uint32_t v_s, int n) {
   const int tid = threadIdx.x & 127, lane = tid & 31, group = (threadIdx.x >> 7) & 1;
-  constexpr int kQ = TreeSmem<MT>::kQ;
   // a group's tiles have one stage of their own
   static_assert(kTreeStages == kTreeGroups, "one stage per producer group");
-  const uint32_t kst = k_s + group * kTreeOperand, vst = v_s + group * kTreeOperand;
-  uint4 rk[4][2], rv[4][2];  // the codes of the group's next tile
-  uint32_t fmt = 0;
+  const uint32_t vst = v_s + group * kTreeOperand;
+  const TreeK kp(k_s + group * kTreeOperand, tid);
+  const TreeV vp(vst, tid);
+  // the group's next tile: codes (K of unit c in 4 c, 4 c + 1, V in the next
+  // two) or K rows
+  uint4 x[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) x[i] = make_uint4(0, 0, 0, 0);
 
   // one round per tile of the group, and one before the first that only loads
   for (int j = group - kTreeGroups; j < n; j += kTreeGroups) {
-    const uint32_t ph = (j / kTreeStages) & 1;
     if (j >= 0) {
+      const uint32_t ph = (j / kTreeStages) & 1;
       TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-      const uint32_t flags = r.flags;
-      if (flags & kTileFirst) {
-        const uint32_t seg = flags >> kTileSegShift;
-        if (!tree_wait_warp(sm, &sm.qempty[seg % kQ], ((seg / kQ) & 1) ^ 1, a)) return;
-        load_q<MT>(a, r, q_s + (seg % kQ) * MT * kTreeOperand, tid);
-        producer_arrive(&sm.qfull[seg % kQ], lane);
-      }
-      if (!tree_wait_warp(sm, &sm.kempty[group], ph ^ 1, a)) return;
-      if (kF16 || !(flags & kTileCold)) {
-        // FP16 rows.  V first: the record names the nodes whose V is not
-        // finite.  Such a value must not meet the zero weight of a row that
-        // does not attend its node: it becomes 0 here, and the rows that do
-        // attend the node add it at the end
-        if (!tree_wait_warp(sm, &sm.vempty[group], ph ^ 1, a)) return;
+      const uint32_t flags = r.flags, fmt = r.fmt;
+      if (!tree_wait(sm, &sm.kempty[group], ph ^ 1, a)) return;
+      const bool rows = kF16 || !(flags & kTileCold);
+      if (rows) {
+        if (!(flags & kTileCold)) {
+          // ring rows and nodes, at most two of a unit's tiles
 #pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const __half *p = tree_row(a, r, c, kp.row, 0);
+            if (p) {
+              kp.load_row(p, x + 4 * c);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; i++) x[4 * c + i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; c++) kp.store_row(c, x + 4 * c);
+      } else if constexpr (!kF16) {
+#pragma unroll
+        for (int c = 0; c < 4; c++) kp.store(c, fmt >> c & 1, x + 4 * c);
+      }
+      warp_arrive(&sm.kfull[group], lane);
+      if (!rows && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+      if (!tree_wait(sm, &sm.vempty[group], ph ^ 1, a)) return;
+      if (rows) {
+        const int k0 = 16 * (tid >> 6), c2 = 2 * (tid & 63);
+#pragma unroll 1
         for (int c = 0; c < 4; c++) {
-          const TreeRows x(r, c);
+          // lane k knows key k's row; every thread takes two channels of 16 keys
+          const uint64_t mine = reinterpret_cast<uint64_t>(tree_row(a, r, c, lane, 1));
           uint32_t w[16];
-          rows_v(a, x, tid, w);
-          if (!kF16 || x.n < 0) {
-            const int k0 = 16 * (tid >> 6);
+#pragma unroll
+          for (int k = 0; k < 16; k++) {
+            const uint64_t p = __shfl_sync(0xffffffffu, mine, k0 + k);
+            w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + c2)) : 0u;
+          }
+          if (!(flags & kTileCold)) {
+            // A node's V that is not finite must not meet the zero weight of a
+            // row that does not attend the node: it becomes 0 here and the
+            // record names the node; the rows that do attend it add it at the
+            // end
+            const int ring = r.hot - (r.row0 + 32 * c + k0);  // ring rows among the 16
             uint32_t b = 0;
 #pragma unroll
             for (int k = 0; k < 16; k++) {
-              const bool lo = f16_not_finite(w[k]), hi = f16_not_finite(w[k] >> 16);
-              if ((lo || hi) && x.r0 + k0 + k >= r.hot) {
-                if (lo) w[k] &= 0xffff0000u;
-                if (hi) w[k] &= 0x0000ffffu;
-                b |= 1u << (k0 + k);
-              }
+              uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
+              if (k < ring) nf = 0;
+              w[k] &= ~((nf >> 15) * 0xffffu);
+              b |= nf ? 1u << k : 0u;
             }
-            b = __reduce_or_sync(0xffffffffu, b);
+            b = __reduce_or_sync(0xffffffffu, b << k0);
             if (lane == 0) r.bad[tid >> 5][c] = b;
           }
           store_v16(vst, c, tid, w);
         }
-        producer_arrive(&sm.vfull[group], lane);
-#pragma unroll
-        for (int c = 0; c < 4; c++) {
-          uint4 k[4];
-          rows_k(a, TreeRows(r, c), tid, k);
-          store_k16(kst, c, tid, k);
-        }
-        producer_arrive(&sm.kfull[group], lane);
-        if (lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
       } else if constexpr (!kF16) {
 #pragma unroll
-        for (int c = 0; c < 4; c++) store_k8(kst, c, tid, fmt >> c & 1, rk[c]);
-        producer_arrive(&sm.kfull[group], lane);
-        if (lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
-        if (!tree_wait_warp(sm, &sm.vempty[group], ph ^ 1, a)) return;
-#pragma unroll
-        for (int c = 0; c < 4; c++) store_v8(vst, c, tid, fmt >> c & 1, rv[c]);
-        producer_arrive(&sm.vfull[group], lane);
+        for (int c = 0; c < 4; c++) vp.store(c, fmt >> c & 1, x + 4 * c + 2);
       }
+      warp_arrive(&sm.vfull[group], lane);
+      if (rows && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
     }
-    // the group's next tile: its codes have the time of two tiles to come
+    // the group's next tile: it has the time of two tiles to come
     const int next = j + kTreeGroups;
     if (next >= n) break;
     if (next % kTreeBatch < kTreeGroups) {
       const int batch = next / kTreeBatch;
-      if (!tree_wait_warp(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) return;
+      if (!tree_wait(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) return;
     }
     const TreeRec &r = sm.rec[next & (kTreeRecs - 1)];
-    if (!kF16) {
-      const bool cold = r.flags & kTileCold;
-      fmt = r.fmt;
+    if (r.flags & kTileCold) {
+      const uint32_t fmt = r.fmt;
 #pragma unroll
       for (int c = 0; c < 4; c++) {
-        const uint8_t *pair = cold ? r.at[c] : nullptr;
-        if (pair) {
-          load_k(a, pair, fmt >> (4 + c) & 1, fmt >> c & 1, tid, rk[c]);
-          load_v(a, pair, fmt >> (4 + c) & 1, fmt >> c & 1, tid, rv[c]);
-        } else {  // code 0
-          rk[c][0] = rk[c][1] = rv[c][0] = rv[c][1] = make_uint4(0, 0, 0, 0);
+        const uint8_t *at = r.at[c];
+        if (!at) {  // a unit without keys: its logits are masked, its weights 0
+#pragma unroll
+          for (int i = 0; i < 4; i++) x[4 * c + i] = make_uint4(0, 0, 0, 0);
+        } else if constexpr (kF16) {
+          kp.load_row(reinterpret_cast<const __half *>(at) + 2 * kp.row * kDim, x + 4 * c);
+        } else {
+          kp.load(at, fmt >> (4 + c) & 1, fmt >> c & 1, x + 4 * c);
+          vp.load(at, fmt >> (4 + c) & 1, fmt >> c & 1, x + 4 * c + 2);
         }
       }
+    } else {  // (nothing of the last tile lives on)
+#pragma unroll
+      for (int i = 0; i < 16; i++) x[i] = make_uint4(0, 0, 0, 0);
     }
   }
 }
 
 // ---- the scout ----
+
+// [p, p + bytes) on its way into L2; 16-byte aligned.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// The query rows of a unit into its Q operand(s), one arrival per lane when they
+// are there (rows beyond the tree keep what they were: nobody reads their
+// results).
+template <int MT>
+__device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg, int rows, uint32_t st, uint64_t *bar,
+                                        int lane) {
+  const int G = a.group, n = min(128 * MT, rows - mg * 128 * MT), c = lane & 15;
+  const __half *q = a.q + (static_cast<size_t>(b) * a.max_tree * a.hq + hk * G) * kDim + 8 * c;
+  const uint32_t to = st + (c >> 3) * kTreeSlab;
+#pragma unroll 2
+  for (int r = lane >> 4; r < n; r += 2) {
+    const int row = mg * 128 * MT + r, t = row_node(a, row);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     to + (r >> 7) * kTreeOperand + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                 "l"(q + (static_cast<size_t>(t) * a.hq + row - t * G) * kDim)
+                 : "memory");
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Lane 4 k + c looks up unit c of tile k of a batch.
 template <int MT, bool kF16>
-__device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, int n) {
+__device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, int n) {
+  constexpr int kQ = TreeSmem<MT>::kQ;
   const int lane = threadIdx.x & 31, k = (lane >> 2) & (kTreeBatch - 1), c = lane & 3;
   const bool on = lane < 4 * kTreeBatch;
   int b = sm.start_b, segs = 0;     // segments begun before the batch
   TreeSeq q = tree_seq<MT>(a, b);
   long long pos = sm.start_pos + k; // the lane's tile within sequence b
+  uint32_t q_use = 0, q_count = 0;  // Q buffer i, stream s: bit 2 i + s in use; byte 2 i + s: its phases so far
+
   for (int j0 = 0, batch = 0; j0 < n; j0 += kTreeBatch, batch++) {
     const int j = j0 + k;
     const bool have = on && j < n;
@@ -539,11 +498,12 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       unit = static_cast<int>(pos / q.tiles);
       t = static_cast<int>(pos - static_cast<long long>(unit) * q.tiles);
     }
-    const int in = min(t, j);  // tiles of the segment before this one
+    const int in = min(t, j);                        // tiles of the segment before this one
+    const int left = min(q.tiles - 1 - t, n - 1 - j);  // and after it
     const uint32_t firsts = __ballot_sync(0xffffffffu, have && in == 0 && c == 0);
     const int seg = segs + __popc(firsts & (0xffffffffu >> (31 - (4 * k)))) - 1;
-    segs += __popc(firsts);
-    const int hk = unit / q.groups, mg = unit - hk * q.groups;
+    const int hk = unit / q.groups, mg = unit - hk * q.groups, rows = q.nt * a.group;
+
     const int p = t * kTK + 32 * c;  // the unit's first position
     const bool cold = t * kTK < q.cold;
     int valid = cold ? max(0, min(32, q.cold - p)) : 0;
@@ -563,9 +523,9 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
           prefetch_l2(at, 32 * kHotTokenBytes);
         } else {
           at = a.cold + ((i << a.lsub) + (slot >> 6)) * kTilePairBytes;
+          sc = __ldg(reinterpret_cast<const float2 *>(a.scales) + i);
           if (a.quant_bits == 4 || (a.n_int4 != nullptr && block < a.n_int4[b])) fmt |= 1;
           if (slot & 32) fmt |= 16;
-          sc = __ldg(reinterpret_cast<const float2 *>(a.scales) + i);
           if (!(slot & 32)) {  // the unit with the first slots brings the tile pair
             if (fmt & 1) {
               prefetch_l2(at, kTileBytes / 2);
@@ -591,7 +551,7 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, o));
       fmt |= __shfl_xor_sync(0xffffffffu, fmt, o);
     }
-    if (!tree_wait_warp(sm, &sm.rfree[batch & 1], ((batch >> 1) & 1) ^ 1, a)) return;
+    if (!tree_wait(sm, &sm.rfree[batch & 1], ((batch >> 1) & 1) ^ 1, a)) return;
     if (have) {
       TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
       r.at[c] = at;
@@ -601,161 +561,123 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       if (c == 0) {
         r.fmt = fmt;
         r.v_max = v_max;
-        const int rows = MT == 1 ? 1 : min(MT, (q.nt * (a.hq / a.hkv) - mg * 128 * MT + 127) / 128);
-        r.flags = (in == 0 ? kTileFirst : in == 1 ? kTileSecond : 0) |
-                  (t == q.tiles - 1 || j == n - 1 ? kTileLast : 0) | (plain ? kTilePlain : 0) | (cold ? kTileCold : 0) |
-                  static_cast<uint32_t>(rows) << kTileRowsShift | static_cast<uint32_t>(seg & 3) << kTileSegShift;
+        r.flags = (in == 0 ? kTileFirst : in == 1 ? kTileSecond : 0) | (left == 0 ? kTileLast : 0) |
+                  (plain ? kTilePlain : 0) | (cold ? kTileCold : 0) | (t <= j ? kUnitStart : 0) |
+                  (left == q.tiles - 1 - t ? kUnitEnd : 0) | static_cast<uint32_t>(seg & 3) << kTileSegShift;
+        r.left = left;
+        r.rest = q.tiles - 1 - t;
         r.b = b;
         r.hk = hk;
         r.mg = mg;
+        r.rows = rows;
+        r.row0 = row0;
         r.cold = q.cold;
         r.hot = q.hot;
         r.keys = q.keys;
-        r.row0 = row0;
+        r.ring = reinterpret_cast<const __half *>(a.hot) + (static_cast<size_t>(b) * a.hkv + hk) * a.hot_tokens * 2 * kDim;
+        const size_t first_node = (static_cast<size_t>(b) * a.max_tree * a.hkv + hk) * kDim;
+        r.node[0] = a.k_tree + first_node;
+        r.node[1] = a.v_tree + first_node;
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.rfull[batch & 1]);
+    warp_arrive(&sm.rfull[batch & 1], lane);
+    // the segments that begin in this batch: their query rows
+    for (uint32_t f = firsts; f; f &= f - 1, segs++) {
+      const int s = segs;
+      const int from = __ffs(f) - 1, i = s % kQ;
+      const int fb = __shfl_sync(0xffffffffu, b, from), fhk = __shfl_sync(0xffffffffu, hk, from);
+      const int fmg = __shfl_sync(0xffffffffu, mg, from), frows = __shfl_sync(0xffffffffu, rows, from);
+      const int fleft = __shfl_sync(0xffffffffu, left, from), fj = __shfl_sync(0xffffffffu, j, from);
+      for (int st = 0; st < 2; st++) {  // the streams that read the buffer last
+        const int at = 2 * i + st;
+        if (!(q_use >> at & 1)) continue;
+        if (!tree_wait(sm, &sm.qempty[i][st], ((q_count >> (8 * at) & 1) ^ 1), a)) return;
+        q_use &= ~(1u << at);
+      }
+      for (int st = 0; st < 2; st++)
+        if (MT == 2 || fleft > 0 || (fj & 1) == st) {
+          const int at = 2 * i + st;
+          q_use |= 1u << at;
+          q_count = (q_count & ~(255u << (8 * at))) | (((q_count >> (8 * at)) + 1) & 255u) << (8 * at);
+        }
+      fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * MT * kTreeOperand, &sm.qfull[i], lane);
+    }
     pos += kTreeBatch;
   }
 }
 
-// ---- the MMA warp (one elected thread issues) ----
+// ---- the MMA warps (one elected thread issues) ----
 // TMEM columns: S of stream i at 128 i, its O at 256 + 128 i.  The weights of a
-// tile replace its S (FP16, the first 64 columns).
-
-// S of tile j for stream i; its Q operand is number `q`
-template <int MT>
-__device__ __forceinline__ void tree_qk(TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t tmem, int j, int i, int q) {
-  const uint64_t dq = tc_desc_sw128(q_s + q * kTreeOperand);
-  const uint64_t dk = tc_desc_sw128(k_s + (j & (kTreeStages - 1)) * kTreeOperand);
-  if (tc_elect()) {
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-      const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
-      tc_mma_ss(tmem + 128 * i, dq + o, dk + o, tc_idesc_f16(128), k > 0);
-    }
-    tc_commit(&sm.sfull[i]);
-  }
-  __syncwarp();
-}
-
-// O += P V of tile j for stream i, whose n-th tile it is
-template <int MT>
-__device__ __forceinline__ bool tree_pv(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t v_s, uint32_t tmem, int j, int i,
-                                        int n, bool first) {
-  if (!tree_wait_warp(sm, &sm.vfull[j & (kTreeStages - 1)], (j / kTreeStages) & 1, a)) return false;
-  if (!tree_wait_warp(sm, &sm.pfull[i], n & 1, a)) return false;
-  fence_proxy_async_smem();
-  tc_fence_after();
-  const uint64_t dv = tc_desc_sw128(v_s + (j & (kTreeStages - 1)) * kTreeOperand);
-  if (tc_elect()) {
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-      const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
-      tc_mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, dv + o, tc_idesc_f16(128), !first || k > 0);
-    }
-    tc_commit(&sm.odone[i]);
-  }
-  __syncwarp();
-  return true;
-}
+// tile replace the upper half of its S (FP16, 64 columns).
 
 template <int MT>
 __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
-                                         uint32_t tmem, int n) {
+                                         uint32_t tmem, int n, int i) {
   constexpr int kQ = TreeSmem<MT>::kQ;
-  auto commit = [](uint64_t *bar) {
-    if (tc_elect()) tc_commit(bar);
-    __syncwarp();
-  };
-  auto two = [](uint32_t flags) { return MT == 2 && ((flags >> kTileRowsShift) & 3) == 2; };
-  // tile j's K is there, and its segment's Q
-  auto open = [&](int j, uint32_t &flags) -> bool {
-    if (!tree_wait_warp(sm, &sm.kfull[j & (kTreeStages - 1)], (j / kTreeStages) & 1, a)) return false;
-    flags = sm.rec[j & (kTreeRecs - 1)].flags;
-    if (flags & kTileFirst) {
-      const uint32_t seg = flags >> kTileSegShift;
-      if (!tree_wait_warp(sm, &sm.qfull[seg % kQ], (seg / kQ) & 1, a)) return false;
-    }
+  constexpr uint32_t idesc = tc_idesc_f16(128);
+  const uint32_t t_s = tmem + 128 * i, t_p = t_s + 64, t_o = tmem + 256 + 128 * i;
+  int used = 0, begun = 0;  // tiles and segments of the stream
+  for (int j = MT == 1 ? i : 0; j < n; j += MT == 1 ? 2 : 1, used++) {
+    const int s = j & (kTreeStages - 1);
+    const uint32_t ph = (j / kTreeStages) & 1;
+    // S = Q K^T (it replaces the weights of the stream's last P V)
+    if (!tree_wait(sm, &sm.kfull[s], ph, a)) return;
+    const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
+    const uint32_t flags = r.flags, seg = flags >> kTileSegShift;
+    const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
+    const bool last = MT == 1 ? r.left < 2 : flags & kTileLast;
+    if (first && !tree_wait(sm, &sm.qfull[seg % kQ], (seg / kQ) & 1, a)) return;
     fence_proxy_async_smem();
     tc_fence_after();
-    return true;
-  };
-  auto close = [&](int j, uint32_t flags) {
-    commit(&sm.kempty[j & (kTreeStages - 1)]);
-    if (flags & kTileLast) commit(&sm.qempty[(flags >> kTileSegShift) % kQ]);
-  };
-  auto q_of = [](uint32_t flags) { return static_cast<int>((flags >> kTileSegShift) % kQ) * MT; };
-
-  if (MT == 1) {
-    // tile j belongs to stream j & 1; its Q K^T is issued as soon as the
-    // stream's last P V, whose weights its S overwrites
-    uint32_t f0 = 0, f1 = 0, f2 = 0;  // flags of tiles j, j + 1, j + 2
-    int freed = 0;                    // segments whose O may be written
-    if (!open(0, f0)) return;
-    tree_qk<MT>(sm, q_s, k_s, tmem, 0, 0, q_of(f0));
-    close(0, f0);
-    if (n > 1) {
-      if (!open(1, f1)) return;
-      tree_qk<MT>(sm, q_s, k_s, tmem, 1, 1, q_of(f1));
-      close(1, f1);
+    {
+      const uint64_t dq = tc_desc_sw128(q_s + ((seg % kQ) * MT + (MT == 2 ? i : 0)) * kTreeOperand);
+      const uint64_t dk = tc_desc_sw128(k_s + s * kTreeOperand);
+      if (tc_elect()) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
+          tc_mma_ss(t_s, dq + o, dk + o, idesc, k > 0);
+        }
+        tc_commit(&sm.sfull[i]);
+        tc_commit(&sm.kempty[s]);
+        if (last) tc_commit(&sm.qempty[seg % kQ][i]);
+      }
+      __syncwarp();
     }
-    for (int j = 0; j < n; j++) {
-      if (f0 & kTileFirst) {
-        if (!tree_wait_warp(sm, &sm.ofree[0], (freed & 1) ^ 1, a)) return;
-        freed++;
-      }
-      if (!tree_pv<MT>(a, sm, v_s, tmem, j, j & 1, j >> 1, f0 & (kTileFirst | kTileSecond))) return;
-      commit(&sm.vempty[j & (kTreeStages - 1)]);
-      if ((j + 1) % kTreeBatch == 0) commit(&sm.rfree[(j / kTreeBatch) & 1]);
-      if (j + 2 < n) {
-        if (!open(j + 2, f2)) return;
-        tree_qk<MT>(sm, q_s, k_s, tmem, j + 2, j & 1, q_of(f2));
-        close(j + 2, f2);
-      }
-      f0 = f1;
-      f1 = f2;
+    // O += P V
+    if (first) {
+      if (!tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
+      begun++;
     }
-  } else {
-    uint32_t fq = 0, fp;                       // of the tiles of Q K^T (one ahead) and of P V
-    int used0 = 0, used1 = 0, o0 = 0, o1 = 0;  // tiles and segments of row tiles 0 and 1
-    if (!open(0, fq)) return;
-    tree_qk<MT>(sm, q_s, k_s, tmem, 0, 0, q_of(fq));
-    if (two(fq)) tree_qk<MT>(sm, q_s, k_s, tmem, 0, 1, q_of(fq) + 1);
-    close(0, fq);
-    for (int j = 0; j < n; j++) {
-      fp = fq;
-      const bool more = j + 1 < n, first = fp & kTileFirst;
-      if (first) {
-        if (!tree_wait_warp(sm, &sm.ofree[0], (o0++ & 1) ^ 1, a)) return;
-        if (two(fp) && !tree_wait_warp(sm, &sm.ofree[1], (o1++ & 1) ^ 1, a)) return;
+    if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
+    if (!tree_wait(sm, &sm.pfull[i], used & 1, a)) return;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    const uint64_t dv = tc_desc_sw128(v_s + s * kTreeOperand);
+    const bool batch_end = MT == 1 ? (j + 2) / kTreeBatch != j / kTreeBatch : (j + 1) % kTreeBatch == 0;
+    if (tc_elect()) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
+        tc_mma_ts(t_o, t_p + 8 * k, dv + o, idesc, !first || k > 0);
       }
-      // the next tile's S of a row tile follows that row tile's P V
-      if (!tree_pv<MT>(a, sm, v_s, tmem, j, 0, used0++, first)) return;
-      if (more) {
-        if (!open(j + 1, fq)) return;
-        tree_qk<MT>(sm, q_s, k_s, tmem, j + 1, 0, q_of(fq));
-      }
-      if (two(fp) && !tree_pv<MT>(a, sm, v_s, tmem, j, 1, used1++, first)) return;
-      commit(&sm.vempty[j & (kTreeStages - 1)]);
-      if ((j + 1) % kTreeBatch == 0) commit(&sm.rfree[(j / kTreeBatch) & 1]);
-      if (more) {
-        if (two(fq)) tree_qk<MT>(sm, q_s, k_s, tmem, j + 1, 1, q_of(fq) + 1);
-        close(j + 1, fq);
-      }
+      tc_commit(&sm.vempty[s]);
+      if (last) tc_commit(&sm.odone[i]);
+      if (batch_end) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
     }
+    __syncwarp();
   }
 }
 
 // ---- softmax ----
 
-__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t *v) {
   float m[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) m[k] = __uint_as_float(v[k]);
 #pragma unroll
-  for (int k = 4; k < 32; k++) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(v[k]));
+  for (int k = 4; k < N; k++) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(v[k]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -790,35 +712,22 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
 
 // The nodes of unit c of a tail tile that the row attends (bits), k = the node
 // of the unit's first key; `odd` collects those whose V is not finite.
-__device__ __forceinline__ uint32_t tree_nodes(const TreeRec &me, int c, int k, uint64_t nodes, uint64_t &odd) {
+__device__ __forceinline__ uint32_t tree_nodes(const TreeRec &r, int c, int k, uint64_t nodes, uint64_t &odd) {
   uint32_t own = 0, bad = 0;
   if (k >= 0) own = k < 64 ? static_cast<uint32_t>(nodes >> k) : 0u;
   else if (k > -32) own = static_cast<uint32_t>(nodes << -k);
 #pragma unroll
-  for (int w = 0; w < 4; w++) bad |= me.bad[w][c];
+  for (int w = 0; w < 4; w++) bad |= r.bad[w][c];
   bad &= own;
   if (bad) odd |= k >= 0 ? static_cast<uint64_t>(bad) << k : static_cast<uint64_t>(bad) >> -k;
   return own;
 }
 
 // 16 channels of a row, from channel c0 on: to the output, or to the CTA's part
-// of a unit that several share.  v: the sums in units of `scale`.
+// of a unit that several share.
 template <int MT>
-__device__ __forceinline__ void tree_store(const TreeArgs &a, uint32_t (&v)[16], float scale, uint64_t odd, int c0, int b,
-                                           int hk, bool live, bool whole, size_t out_row, size_t slot, int part_row) {
-#pragma unroll
-  for (int k = 0; k < 16; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) * scale);
-  for (uint64_t rest = odd; rest; rest &= rest - 1) {
-    const int node = __ffsll(static_cast<long long>(rest)) - 1;
-    const __half *vr = a.v_tree + ((static_cast<size_t>(b) * a.max_tree + node) * a.hkv + hk) * kDim + c0;
-#pragma unroll
-    for (int k = 0; k < 16; k += 2) {
-      const __half2 x = *reinterpret_cast<const __half2 *>(vr + k);
-      if (f16_not_finite(__half_as_ushort(x.x))) v[k] = __float_as_uint(__uint_as_float(v[k]) + __low2float(x));
-      if (f16_not_finite(__half_as_ushort(x.y))) v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + __high2float(x));
-    }
-  }
-  if (!live) return;
+__device__ __forceinline__ void tree_store(const TreeArgs &a, const uint32_t (&v)[16], int c0, bool whole, size_t out_row,
+                                           size_t slot, int part_row) {
   if (whole) {
 #pragma unroll
     for (int k = 0; k < 16; k += 8) {
@@ -836,199 +745,215 @@ __device__ __forceinline__ void tree_store(const TreeArgs &a, uint32_t (&v)[16],
   }
 }
 
+// The values of V that are not finite, of the attended nodes `odd`, join the
+// channels [c0, c1) that tree_store wrote: rare, and small rather than fast.
 template <int MT>
-__device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t tmem, int n_tiles) {
+__device__ __forceinline__ void tree_store_odd(const TreeArgs &a, uint64_t odd, int c0, int c1, int b, int hk, bool whole,
+                                            size_t out_row, size_t slot, int part_row) {
+  for (; odd; odd &= odd - 1) {
+    const int node = __ffsll(static_cast<long long>(odd)) - 1;
+    const __half *v = a.v_tree + ((static_cast<size_t>(b) * a.max_tree + node) * a.hkv + hk) * kDim;
+#pragma unroll 1
+    for (int c = c0; c < c1; c++) {
+      if (!f16_not_finite(__half_as_ushort(v[c]))) continue;
+      __half *o = a.out + out_row * kDim + c;
+      float *p = a.part_o + ((slot * 32 + c / 4) * 128 * MT + part_row) * 4 + c % 4;
+      if (whole) *o = __float2half_rn(__half2float(*o) + __half2float(v[c]));
+      else *p += __half2float(v[c]);
+    }
+  }
+}
+
+template <int MT>
+__device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t tmem, int n) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stream = warp >> 2, row_in = threadIdx.x & 127;
   const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  const uint32_t t_s = lanes + 128 * stream, t_o = lanes + 256 + 128 * stream;
-  const int G = a.hq / a.hkv;
-  TreeWalk<MT> walk;
-  walk.pos = sm.start_pos;
-  walk.left = n_tiles;
-  walk.b = sm.start_b;
-  walk.enter(a);
-  int j = 0;      // tiles of the CTA so far
-  int mine = 0;   // tiles of this stream so far
-  for (int seg = 0; walk.next(a); seg++) {
-    const int j0 = j;
-    j += walk.t1 - walk.t0;
-    if (MT == 2 && stream >= walk.m_tiles(a)) continue;
-    const int row = walk.mg * 128 * MT + (MT == 2 ? stream * 128 : 0) + row_in;
-    const bool live = row < walk.nt * G;
-    const bool warp_live = row - lane < walk.nt * G;
-    const int t = live ? row / G : 0;
-    const int cold_tiles = (walk.cold + kTK - 1) / kTK;
-    uint64_t nodes = 0;  // nodes this row attends
-    int node0 = 0;       // the node of the first tail row
-    {
-      const TreeSeq seq = tree_seq<MT>(a, walk.b);
-      node0 = -seq.hot;
-      if (live && seq.keys > 0) {
-        nodes = a.mask ? a.mask[static_cast<size_t>(walk.b) * a.max_tree + t] : (~0ull >> (63 - t));
-        if (seq.keys < 64) nodes &= (1ull << seq.keys) - 1;
-      }
+  const uint32_t t_s = lanes + 128 * stream, t_p = t_s + 64, t_o = lanes + 256 + 128 * stream;
+  const int part_row = (MT == 2 ? stream * 128 : 0) + row_in;
+  // the row's state in the segment
+  uint64_t odd = 0;  // attended nodes whose V is not finite
+  float m = -INFINITY, l = 0.f, ref = 1.f;
+  int ends = 0;      // segments of the stream, and of those the merged ones (upper half)
+  uint32_t used = 0; // tiles of the stream
+
+  for (int j = MT == 1 ? stream : 0; j < n; j += MT == 1 ? 2 : 1, used++) {
+    if (!tree_wait(sm, &sm.sfull[stream], used & 1, a)) return;
+    if (!tree_wait(sm, &sm.mfull[j & (kTreeRecs - 1)], (j / kTreeRecs) & 1, a)) return;
+    tc_fence_after();
+    const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
+    const uint32_t flags = r.flags;
+    const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
+    const int row = r.mg * 128 * MT + part_row;  // of the sequence and kv head
+    const bool live = row < r.rows, warp_live = row - lane < r.rows;
+    if (first) {
+      m = -INFINITY;
+      l = 0.f;
+      odd = 0;
     }
-    float m = -INFINITY, l = 0.f, ref = 1.f, inv = 1.f;
-    uint64_t odd = 0;    // attended nodes whose V is not finite
-    bool first = true;   // of this stream in the segment
-    for (int i = MT == 2 ? j0 : j0 + ((j0 ^ stream) & 1); i < j; i += MT == 2 ? 1 : 2) {
-      // (a row tile that sat out a segment may have missed phases of mfull: S
-      // first, whose phases are its own)
-      if (!tree_wait_warp(sm, &sm.sfull[stream], mine & 1, a)) return;
-      if (!tree_wait_warp(sm, &sm.mfull[i & (kTreeRecs - 1)], (i / kTreeRecs) & 1, a)) return;
-      tc_fence_after();
-      if (warp_live) {
-        const TreeRec &me = sm.rec[i & (kTreeRecs - 1)];
-        const int ti = walk.t0 + i - j0;
-        const bool tail = ti >= cold_tiles, plain = me.flags & kTilePlain;
-        const int k0 = node0 + (ti - cold_tiles) * kTK;
-        float top = -INFINITY;
-        uint32_t v[32];
+    if (warp_live) {
+      const bool tail = !(flags & kTileCold), plain = flags & kTilePlain;
+      // the two halves of S; where keys are masked (or a scale is negative) S
+      // becomes the logits, -inf where masked
+      uint64_t nodes = 0;  // nodes that the row attends
+      if (tail && live && r.keys > 0) {
+        const int t = row_node(a, row);
+        nodes = a.mask ? a.mask[static_cast<size_t>(r.b) * a.max_tree + t] : (~0ull >> (63 - t));
+        if (r.keys < 64) nodes &= (1ull << r.keys) - 1;
+      }
+      float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 4; c++) {
-          tc_ld32(t_s + 32 * c, v);
-          const float s = me.k_scale[c] * a.qk_scale;
-          tc_wait_ld(v);
-          if (plain) {
-            top = fmaxf(top, max32(v) * s);
-          } else {
-            uint32_t ok = me.ok[c];
-            if (tail) ok |= tree_nodes(me, c, k0 + 32 * c, nodes, odd);
+      for (int h = 0; h < 2; h++) {
+        uint32_t v[64];
+        tc_ld64(t_s + 64 * h, v);
+        tc_wait_ld(v);
+        float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
+        if (!plain) {
+          uint32_t ok0 = r.ok[2 * h], ok1 = r.ok[2 * h + 1];
+          if (tail) {
+            const int k = r.row0 - r.hot + 64 * h;
+            ok0 |= tree_nodes(r, 2 * h, k, nodes, odd);
+            ok1 |= tree_nodes(r, 2 * h + 1, k + 32, nodes, odd);
+          }
 #pragma unroll
-            for (int k = 0; k < 32; k++)
-              if (ok >> k & 1) top = fmaxf(top, __uint_as_float(v[k]) * s);
+          for (int k = 0; k < 32; k++) {
+            v[k] = ok0 >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * s0) : 0xff800000u;
+            v[k + 32] = ok1 >> k & 1 ? __float_as_uint(__uint_as_float(v[k + 32]) * s1) : 0xff800000u;
+          }
+          tc_st64(t_s + 64 * h, v);
+          s0 = s1 = 1.f;
+        }
+        top = fmaxf(top, fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1));
+      }
+      if (!plain) tc_wait_st();
+      // m and r follow when they lag too far behind; O and l follow them (the
+      // stream's last P V is done: this tile's S came after it)
+      const float v_max = r.v_max;
+      float ref_new = first ? 1.f : ref;
+      if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
+      const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
+      if (__any_sync(0xffffffffu, m_new != m || ref_new != ref)) {
+        if (!first) {
+          const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
+          l *= f;
+          const float g = f * __fdividef(ref, ref_new);
+#pragma unroll 1
+          for (int c = 0; c < 8; c++) {
+            uint32_t o[16];
+            tc_ld16(t_o + 16 * c, o);
+            tc_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+            tc_st16(t_o + 16 * c, o);
           }
         }
-        // m and r follow when they lag too far behind; O and l follow them (the
-        // stream's last P V is done: this tile's S came after it)
-        float r_new = ref;
-        const float v_max = me.v_max;
-        if (first || v_max > kLagScale * ref) r_new = v_max > 0.f ? v_max : ref;
-        const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
-        if (__any_sync(0xffffffffu, m_new != m || r_new != ref)) {
-          if (!first) {
-            const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
-            l *= f;
-            const float g = f * __fdividef(ref, r_new);
+        m = m_new;
+        ref = ref_new;
+      }
+      const float inv = __fdividef(1.f, ref);
+      // the weights exp2(logit - m), summed, and times the V scale over the
+      // reference in FP16: they go over the second half of S
+      const float minus_m = m == -INFINITY ? 0.f : -m;
+      const uint64_t b2 = pack2(minus_m, minus_m);
+      uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
-            for (int c = 0; c < 4; c++) {
-              tc_ld32(t_o + 32 * c, v);
-              tc_wait_ld(v);
+      for (int h = 1; h >= 0; h--) {
+        uint32_t v[64], p[32];
+        tc_ld64(t_s + 64 * h, v);
+        tc_wait_ld(v);
 #pragma unroll
-              for (int k = 0; k < 32; k++) v[k] = __float_as_uint(__uint_as_float(v[k]) * g);
-              tc_st32(t_o + 32 * c, v);
-            }
-          }
-          m = m_new;
-          ref = r_new;
-          inv = __fdividef(1.f, ref);
-        }
-        const float base = m == -INFINITY ? 0.f : -m;
-        uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll 1
-        for (int c = 0; c < 4; c++) {
-          tc_ld32(t_s + 32 * c, v);
-          const float s = me.k_scale[c] * a.qk_scale, f = me.v_scale[c] * inv;
-          const uint64_t s2 = pack2(s, s), b2 = pack2(base, base), f2 = pack2(f, f);
-          uint32_t ok = 0xffffffffu;
-          if (!plain) {
-            ok = me.ok[c];
-            if (tail) ok |= tree_nodes(me, c, k0 + 32 * c, nodes, odd);
-          }
-          tc_wait_ld(v);
-          uint32_t p[16];
+        for (int u = 0; u < 2; u++) {
+          const float s = plain ? r.k_scale[2 * h + u] * a.qk_scale : 1.f, f = r.v_scale[2 * h + u] * inv;
+          const uint64_t s2 = pack2(s, s), f2 = pack2(f, f);
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             float x, y;
-            unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2, b2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            if (!plain) {
-              x = ok >> k & 1 ? x : 0.f;
-              y = ok >> (k + 1) & 1 ? y : 0.f;
-            }
-            const uint64_t e = pack2(x, y);
+            unpack2(fma2(pack2(__uint_as_float(v[32 * u + k]), __uint_as_float(v[32 * u + k + 1])), s2, b2), x, y);
+            const uint64_t e = pack2(ex2(x), ex2(y));
             if (k & 2) sum1 = add2(sum1, e);
             else sum0 = add2(sum0, e);
             unpack2(mul2(e, f2), x, y);
-            p[k >> 1] = half2_bits(x, y);
+            p[16 * u + (k >> 1)] = half2_bits(x, y);
           }
-          tc_st16(t_s + 16 * c, p);
         }
-        float x, y;
-        unpack2(add2(sum0, sum1), x, y);
-        l += x + y;
-        tc_wait_st();
+        tc_st32(t_p + 32 * h, p);
       }
-      first = false;
-      mine++;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull[stream]);
+      float x, y;
+      unpack2(add2(sum0, sum1), x, y);
+      l += x + y;
+      tc_wait_st();
     }
-    // the segment's end: O of the stream's last tile
-    const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
-    const size_t out_row = (static_cast<size_t>(walk.b) * a.max_tree + t) * a.hq + walk.hk * G + row - t * G;
-    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (walk.t0 == 0 ? 1 : 0);
-    const int part_row = (MT == 2 ? stream * 128 : 0) + row_in;
-    if (!first) {
-      if (!tree_wait_warp(sm, &sm.odone[stream], (mine - 1) & 1, a)) return;
-      tc_fence_after();
-    }
-    if (MT == 2) {
-      if (warp_live) {
-#pragma unroll 1
-        for (int c = 0; c < 8; c++) {
-          uint32_t v[16];
-          tc_ld16(t_o + 16 * c, v);
-          tc_wait_ld(v);
-          tree_store<MT>(a, v, whole ? (l != 0.f ? ref / l : 0.f) : ref, odd, 16 * c, walk.b, walk.hk, live, whole, out_row,
-                         slot, part_row);
-        }
-      }
-    } else {
-      // both streams of a row meet: group i takes channels 64 i.. of the two
-      TreeStat *st = &sm.stat[seg & 1][0][row_in];
+    // what the segment's end needs of the record, which may be gone after pfull
+    const bool end = MT == 1 ? r.left < 2 : flags & kTileLast;
+    const bool merge = MT == 1 && (r.left > 0 || !(flags & kTileFirst));
+    const int b = r.b, hk = r.hk, mg = r.mg, rest = r.rest - r.left;
+    tc_fence_before();
+    warp_arrive(&sm.pfull[stream], lane);
+    if (!end) continue;
+
+    // O of the stream's last tile
+    const bool whole = (flags & kUnitStart) && (flags & kUnitEnd);
+    const int t = row_node(a, row);
+    const size_t out_row = (static_cast<size_t>(b) * a.max_tree + t) * a.hq + hk * a.group + row - t * a.group;
+    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (flags & kUnitStart ? 1 : 0);
+    if (!tree_wait(sm, &sm.odone[stream], ends & 1, a)) return;
+    ends++;
+    tc_fence_after();
+    // both streams of a row meet: stream i takes channels 64 i.. of the two
+    float g = ref, gx = 0.f;  // factors of this stream's O and of the other's
+    int c0 = 0, c1 = kDim;
+    if (MT == 1 && merge) {
+      TreeStat *st = &sm.stat[ends >> 16 & 1][0][row_in];
       st[128 * stream] = TreeStat{m, l, ref, odd};
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.xfull);
-      if (!tree_wait_warp(sm, &sm.xfull, seg & 1, a)) return;
+      warp_arrive(&sm.xfull, lane);
+      if (!tree_wait(sm, &sm.xfull, ends >> 16 & 1, a)) return;
+      ends += 1 << 16;
       tc_fence_after();
-      if (warp_live) {
-        const TreeStat o = st[128 * (stream ^ 1)];
-        const float top = fmaxf(m, o.m);
-        const float f = m == top ? 1.f : ex2(m - top), fo = o.m == top ? 1.f : ex2(o.m - top);
-        // (a stream without a tile has nothing in its O)
-        const bool other = walk.t1 - walk.t0 > 1 || first;
-        l = l * f + o.l * fo;
-        m = top;
-        const float scale = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
-        const float g = first || f == 0.f ? 0.f : f * ref, go = !other || fo == 0.f ? 0.f : fo * o.ref;
-        const uint32_t t_o2 = lanes + 256 + 128 * (stream ^ 1);
-#pragma unroll 1
-        for (int c = 4 * stream; c < 4 * stream + 4; c++) {
-          uint32_t v[16];
-          if (!first) {
-            tc_ld16(t_o + 16 * c, v);
-            tc_wait_ld(v);
-          }
-#pragma unroll
-          for (int k = 0; k < 16; k++) v[k] = g == 0.f ? 0u : __float_as_uint(__uint_as_float(v[k]) * g);
-          if (other) {
-            uint32_t w[16];
-            tc_ld16(t_o2 + 16 * c, w);
-            tc_wait_ld(w);
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-              if (go != 0.f) v[k] = __float_as_uint(fmaf(__uint_as_float(w[k]), go, __uint_as_float(v[k])));
-          }
-          tree_store<MT>(a, v, scale, odd | o.odd, 16 * c, walk.b, walk.hk, live, whole, out_row, slot, part_row);
-        }
-      }
+      const TreeStat x = st[128 * (stream ^ 1)];
+      const float top = fmaxf(m, x.m);
+      const float f = m == top ? 1.f : ex2(m - top), fx = x.m == top ? 1.f : ex2(x.m - top);
+      l = l * f + x.l * fx;
+      m = top;
+      odd |= x.odd;
+      g *= f;
+      gx = fx * x.ref;
+      c0 = 64 * stream;
+      c1 = c0 + 64;
     }
-    if (live && (MT == 2 || stream == 0)) {
+    const bool writer = c0 == 0;
+    if (warp_live) {
+      const float scale = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+      g *= scale;
+      gx *= scale;
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 16) {
+        uint32_t o[16];
+        tc_ld16(t_o + c, o);
+        tc_wait_ld(o);
+#pragma unroll
+        for (int k = 0; k < 16; k++) o[k] = g != 0.f ? __float_as_uint(__uint_as_float(o[k]) * g) : 0u;
+        if (MT == 1 && merge) {
+          uint32_t w[16];
+          tc_ld16(lanes + 256 + 128 * (stream ^ 1) + c, w);
+          tc_wait_ld(w);
+#pragma unroll
+          for (int k = 0; k < 16; k++)
+            if (gx != 0.f) o[k] = __float_as_uint(fmaf(__uint_as_float(w[k]), gx, __uint_as_float(o[k])));
+        }
+        if (live) tree_store<MT>(a, o, c, whole, out_row, slot, part_row);
+      }
+      if (live && odd) tree_store_odd<MT>(a, odd, c0, c1, b, hk, whole, out_row, slot, part_row);
+    }
+    // O is free: eight arrivals on its barrier, of both streams' warps or twice
+    // of this one's
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.ofree[stream]);
+      mbar_arrive(&sm.ofree[merge ? stream ^ 1 : stream]);
+    }
+    if (live && writer) {
       if (whole) {
         if (a.lse_out) a.lse_out[out_row] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
@@ -1036,18 +961,11 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         ml[part_row] = make_float2(m, l);
       }
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.ofree[MT == 2 ? stream : 0]);
-    // who has the unit's tiles, from the CTA with its first
-    if (threadIdx.x == 0 && walk.t0 == 0) {
+    // the run's last unit goes on in later CTAs: the merge finds it here
+    if (row_in == 0 && (MT == 1 || stream == 0) && writer && (flags & kUnitStart) && !(flags & kUnitEnd)) {
       const long long ctas = min(static_cast<long long>(a.ctas), sm.total);
-      // the list's index of the unit's last tile, and the run that has it
-      const long long end = sm.total * blockIdx.x / ctas + j0 + walk.tiles;
-      const int last = static_cast<int>((end * ctas - 1) / sm.total);
-      const int groups_max = (a.max_tree * G + 128 * MT - 1) / (128 * MT);
-      a.unit_ctas[(static_cast<size_t>(walk.b) * a.hkv + walk.hk) * groups_max + walk.mg] =
-          make_int2(static_cast<int>(blockIdx.x), last);
+      const long long end = sm.total * (blockIdx.x + 1) / ctas + rest;  // of the unit, in the list
+      a.shared_units[blockIdx.x] = make_int4(b, hk, mg, static_cast<int>((end * ctas - 1) / sm.total - blockIdx.x));
     }
   }
 }
@@ -1062,7 +980,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                                                        2 * kTreeStages * kTreeOperand);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
-  constexpr int kMmaWarp = kTreeSoft + kTreeProd;
+  constexpr int kMmaWarp = kTreeSoft + kTreeProd, kScoutWarp = kMmaWarp + kTreeMma;
 
   // the list's length and where this CTA's run starts: every thread sums a
   // range of sequences, a scan over the threads places them
@@ -1082,30 +1000,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   }
   if (lane == 31) sm.warp_sum[warp] = inc;
   if (tid == 0) {
+    a.shared_units[blockIdx.x] = make_int4(0, 0, 0, 0);
     sm.abort = 0;
-    for (int i = 0; i < kTreeStages; i++) {
-      mbar_init(&sm.kfull[i], kTreeProd / kTreeGroups);
-      mbar_init(&sm.kempty[i], 1);
-      mbar_init(&sm.vfull[i], kTreeProd / kTreeGroups);
-      mbar_init(&sm.vempty[i], 1);
-    }
-    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd / kTreeGroups);
-    for (int i = 0; i < TreeSmem<MT>::kQ; i++) {
-      mbar_init(&sm.qfull[i], kTreeProd / kTreeGroups);
-      mbar_init(&sm.qempty[i], 1);
-    }
     for (int i = 0; i < 2; i++) {
+      mbar_init(&sm.kfull[i], kTreeProd / kTreeGroups);
+      mbar_init(&sm.vfull[i], kTreeProd / kTreeGroups);
+      mbar_init(&sm.kempty[i], MT);
+      mbar_init(&sm.vempty[i], MT);
+      mbar_init(&sm.rfull[i], 1);
+      mbar_init(&sm.rfree[i], 2);
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.pfull[i], 4);
       mbar_init(&sm.odone[i], 1);
-      mbar_init(&sm.ofree[i], MT == 1 ? 8 : 4);
+      mbar_init(&sm.ofree[i], 8);
+      mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.rfull[i], 1);
-      mbar_init(&sm.rfree[i], 1);
+    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd / kTreeGroups);
+    for (int i = 0; i < TreeSmem<MT>::kQ; i++) {
+      mbar_init(&sm.qfull[i], 32);
+      mbar_init(&sm.qempty[i][0], 1);
+      mbar_init(&sm.qempty[i][1], 1);
     }
     mbar_init(&sm.xfull, 8);
-    mbar_init(&sm.drain, 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -1141,21 +1057,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   const uint32_t tmem = sm.tmem;
 
   if (warp < kTreeSoft) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeSoftRegs));
     tree_softmax<MT>(a, sm, tmem, n_tiles);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeProdRegs));
-    tree_produce<MT, kF16>(a, sm, q_s, k_s, v_s, n_tiles);
-  } else if (warp > kMmaWarp) {
-    tree_scout<MT, kF16>(a, sm, n_tiles);
-  } else {
-    tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles);
+    tree_produce<MT, kF16>(a, sm, k_s, v_s, n_tiles);
+  } else if (warp < kScoutWarp) {
+    const int i = warp - kMmaWarp;
+    tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
     __syncwarp();
     // no MMA is in flight when TMEM is given back
-    if (tc_elect()) tc_commit(&sm.drain);
+    if (tc_elect()) tc_commit(&sm.drain[i]);
     __syncwarp();
-    if (!mbar_wait_bounded(&sm.drain, 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);
+    if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);
     __syncwarp();
+  } else {
+    tree_scout<MT, kF16>(a, sm, q_s, n_tiles);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -1164,34 +1080,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 }
 
 // ---- the merge of units that several CTAs share ----
-// CTA = (unit, 32 rows): thread = row (lane) and 16 channels (warp); parts in
-// the order of the tiles.
+// CTA = (the CTA with a shared unit's first tile, 32 rows): thread = row (lane)
+// and 16 channels (warp); parts in the order of the tiles.
 template <int MT>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a, int groups_max) {
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int unit = blockIdx.x;
-  const int mg = unit % groups_max, hk = unit / groups_max % a.hkv, b = unit / groups_max / a.hkv;
-  const int G = a.hq / a.hkv;
+  const int c0 = blockIdx.x;
+  const int4 unit = a.shared_units[c0];  // sequence, kv head, row group, tiles of the unit in later CTAs
+  if (unit.w <= 0) return;
+  const int b = unit.x, hk = unit.y, mg = unit.z;
+  const int G = a.group;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nt = a.n_tree ? a.n_tree[b] : a.max_tree;
-  if (nt < 0 || nt > a.max_tree) return;
   const int r = 32 * blockIdx.y + lane, row = mg * 128 * MT + r;
-  if (row - lane >= nt * G) return;
-  const int2 c = a.unit_ctas[unit];
-  // (out of range: a call that gave up before it wrote them)
-  if (c.x < 0 || c.x >= c.y || c.y >= a.ctas || row >= nt * G) return;
+  if (row >= nt * G) return;
   const int t = row / G;
   const size_t out_row = (static_cast<size_t>(b) * a.max_tree + t) * a.hq + hk * G + row - t * G;
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.part_o);
-  float top = -INFINITY;
-  for (int i = c.x; i <= c.y; i++) top = fmaxf(top, ml[(2 * static_cast<size_t>(i) + (i == c.x)) * 128 * MT + r].x);
+  // the later CTAs' parts: all but the last hold nothing else
+  float top = ml[(2 * static_cast<size_t>(c0) + 1) * 128 * MT + r].x;
+  const int c1 = c0 + unit.w;
+  for (int i = c0 + 1; i <= c1; i++) top = fmaxf(top, ml[2 * static_cast<size_t>(i) * 128 * MT + r].x);
   float sum = 0.f;
   float4 o[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = c.x; i <= c.y; i++) {
-    const size_t slot = 2 * static_cast<size_t>(i) + (i == c.x);
+  for (int i = c0; i <= c1; i++) {
+    const size_t slot = 2 * static_cast<size_t>(i) + (i == c0);
     const float2 x = ml[slot * 128 * MT + r];
     const float w = x.x == top ? 1.f : ex2(x.x - top);
     if (x.y == 0.f || w == 0.f) continue;
@@ -1209,9 +1125,8 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   uint32_t h[8];
 #pragma unroll
   for (int k = 0; k < 4; k++) {
-    const __half2 x = __floats2half2_rn(o[k].x * inv, o[k].y * inv), y = __floats2half2_rn(o[k].z * inv, o[k].w * inv);
-    h[2 * k] = *reinterpret_cast<const uint32_t *>(&x);
-    h[2 * k + 1] = *reinterpret_cast<const uint32_t *>(&y);
+    h[2 * k] = half2_bits(o[k].x * inv, o[k].y * inv);
+    h[2 * k + 1] = half2_bits(o[k].z * inv, o[k].w * inv);
   }
   uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * kDim + 16 * warp);
   dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
@@ -1230,21 +1145,15 @@ static cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(tree_kernel<MT, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Shape::kBytes));
     if (e != cudaSuccess) return e;
-    // what the producers add the softmax warps give up, of the registers that
-    // the launch really has
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, tree_kernel<MT, kF16>);
-    if (e != cudaSuccess) return e;
-    if (2 * at.numRegs < kTreeSoftRegs + kTreeProdRegs) return cudaErrorInvalidKernelImage;
     if (dev < 31) configured_dev_mask |= 1 << dev;
   }
   tree_kernel<MT, kF16><<<a.ctas, kTreeThreads, Shape::kBytes, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int G = a.hq / a.hkv, groups = tree_groups(a.max_tree, G);
+  const int G = a.group;
   const int rows = a.max_tree * G < 128 * MT ? a.max_tree * G : 128 * MT;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.batch * a.hkv * groups, (rows + 31) / 32);
+  cfg.gridDim = dim3(a.ctas, (rows + 31) / 32);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -1252,11 +1161,11 @@ static cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<MT>, a, groups);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<MT>, a);
 }
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream) {
-  const bool two = tree_m_tiles(a.max_tree, a.hq / a.hkv) == 2;
+  const bool two = tree_m_tiles(a.max_tree, a.group) == 2;
   if (a.quant_bits == 0) return two ? launch_tree<2, true>(a, stream) : launch_tree<1, true>(a, stream);
   return two ? launch_tree<2, false>(a, stream) : launch_tree<1, false>(a, stream);
 }

@@ -31,6 +31,7 @@ struct TreeArgs {
   float qk_scale;             // softmax_scale * log2(e)
   int group;                  // Hq / Hkv
   int group_recip;            // 2^16 / group, rounded up
+  int q_rows, q_bufs;         // rows of a Q buffer and buffers
   uint32_t wait_cycles;       // limit (SM cycles) of the bounded waits
   int ctas;                   // CTAs of the launch
   // units that several CTAs share (see tree.cu): sums and maxima [2 ctas][rows]

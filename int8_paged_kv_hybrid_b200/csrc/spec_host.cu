@@ -77,6 +77,9 @@ int hyb_tree_attn(const hyb_cache_desc *d, const void *q, const void *k_tree, co
   a.wait_cycles = wait < 0xf0000000ll ? static_cast<uint32_t>(wait) : 0xf0000000u;
   a.ctas = sms;
   a.group = d->num_q_heads / d->num_kv_heads;
+  // two Q buffers where two of 64 rows do
+  a.q_bufs = max_tree * a.group <= 64 ? 2 : 1;
+  a.q_rows = a.q_bufs == 2 ? 64 : 128;
   a.group_recip = 65536 / a.group + 1;
   a.part_o = reinterpret_cast<float *>(ws + w.o);
   a.part_ml = reinterpret_cast<float *>(ws + w.ml);

@@ -22,16 +22,18 @@
 // inside one run is finished there; the others leave (O, m, l) per CTA, and
 // tree_combine_kernel merges them in the order of the tiles.
 //
-// Inside a CTA (19 warps): a scout warp looks the tiles up (block table, scales,
+// Inside a CTA (20 warps): a scout warp looks the tiles up (block table, scales,
 // segment ends) some tiles ahead, writes their records, starts their way into
-// L2 and fetches the query rows; two groups of four producer warps take turns
-// at the tiles and bring codes or rows to FP16 in the 128-byte swizzled layout
-// of the MMA's shared operands; two groups of four softmax warps (one query row
-// per thread) keep two softmax streams and write the weights over the logits in
-// TMEM, where the second product reads them as its A operand; a warp for each
-// stream issues its MMAs.  The streams are the two row tiles (MT 2), or the
-// even and the odd tiles of the run (MT 1), merged at a unit's end; then
-// everything from the stage in shared memory on is one stream's own.
+// L2 and fetches the query rows; a copy warp brings their bytes into a ring in
+// shared memory by bulk copies; eight producer warps turn codes or rows into
+// FP16 in the 128-byte swizzled layout of the MMA's shared operands; two groups
+// of four softmax warps (one query row per thread) keep two softmax streams and
+// write the weights over the logits in TMEM, where the second product reads
+// them as its A operand; a warp for each stream issues its MMAs.  The streams
+// are the two row tiles (MT 2), or the even and the odd tiles of the run (MT
+// 1), merged at a unit's end.  (Codes fetched by the producers' own loads, into
+// registers, made every other warp wait behind them in the load unit: 360 us
+// where this takes a fraction of it.)
 #include "kernels.cuh"
 #include "spec.cuh"
 #include "tc05.cuh"
@@ -44,12 +46,15 @@ constexpr int kTreeBatch = 4;                // tiles the scout looks up at once
 constexpr int kTreeRecs = 2 * kTreeBatch;    // tile records
 constexpr uint32_t kTreeOperand = 128 * 256; // bytes of a 128 x 128 FP16 operand
 constexpr uint32_t kTreeSlab = kTreeOperand / 2;  // its halves of 64 columns
+constexpr uint32_t kTreePiece = 8192;        // a piece of the ring of codes or rows
 constexpr float kLagLog2 = 6.f;
 constexpr float kLagScale = 256.f;
 
-// Warps: softmax, producers, MMA, scout (20 warps of 96 registers fill an SM).
-constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeGroups = 2, kTreeMma = 2;
-constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + kTreeMma + 1);
+// Warps: softmax, producers, MMA, scout, copies: 20 warps of 96 registers at
+// launch; the softmax warps take what the producers do not need.
+constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeMma = 2;
+constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + kTreeMma + 2);
+constexpr int kTreeSoftRegs = 112, kTreeProdRegs = 80;
 
 // TreeRec::flags: the first, the second and the last tile of its segment (the
 // part of a unit that this CTA has); every key attended by every row and no
@@ -65,7 +70,7 @@ struct TreeRec {
   float k_scale[4];      // 1 for FP16 rows
   float v_scale[4];
   uint32_t ok[4];        // keys that every row attends
-  uint32_t bad[4][4];    // [warp][unit]: rows of a tail tile with a V that is not finite (by the producers)
+  uint32_t bad[8];       // keys of unit i / 2 of a tail tile with a V that is not finite (by producer warp i)
   uint32_t fmt;          // bit c: unit c is INT4; bit 4 + c: it is the second half of its slots
   uint32_t flags;
   float v_max;           // largest |v_scale|
@@ -87,13 +92,14 @@ struct TreeStat {
 
 template <int MT>
 struct TreeSmem {
-  static constexpr int kQ = MT == 1 ? 2 : 1;  // Q buffers
+  static constexpr int kPieces = MT == 1 ? 6 : 3;
   // MMA operands: MT 1 stage and stream are one; MT 2 both streams free a stage
   uint64_t kfull[kTreeStages], kempty[kTreeStages], vfull[kTreeStages], vempty[kTreeStages];
+  uint64_t cfull[kPieces], cempty[kPieces];
   uint64_t rfull[2], rfree[2];     // records, by batch parity
   uint64_t mfull[kTreeRecs];       // a record's tile is in shared memory
-  uint64_t qfull[kQ];
-  uint64_t qempty[kQ][2];          // by stream
+  uint64_t qfull[2];
+  uint64_t qempty[2][2];           // by stream
   uint64_t sfull[2], pfull[2], odone[2], ofree[2];  // by stream
   uint64_t xfull;                  // MT 1: both streams' rows are in `stat`
   uint64_t drain[2];
@@ -106,10 +112,14 @@ struct TreeSmem {
   TreeStat stat[MT == 1 ? 2 : 1][MT == 1 ? 2 : 1][MT == 1 ? 128 : 1];  // [parity][stream][row]
 };
 
+// Shared memory: Q, K stages, V stages, pieces, the rest.  MT 1: two buffers of
+// 64 query rows or one of 128 (an MMA reads 128 rows from either: what follows
+// in shared memory makes rows that nobody reads).
 template <int MT>
 struct TreeShape {
-  static constexpr uint32_t kQBytes = TreeSmem<MT>::kQ * MT * kTreeOperand;
-  static constexpr uint32_t kBytes = 1024 + kQBytes + 2 * kTreeStages * kTreeOperand + sizeof(TreeSmem<MT>);
+  static constexpr uint32_t kQBytes = MT * kTreeOperand;
+  static constexpr uint32_t kTiles = kQBytes + 2 * kTreeStages * kTreeOperand;
+  static constexpr uint32_t kBytes = 1024 + kTiles + TreeSmem<MT>::kPieces * kTreePiece + sizeof(TreeSmem<MT>);
 };
 
 // ---- the list of tiles ----
@@ -202,19 +212,44 @@ struct TreeCodec {
   }
 };
 
-// Sixteen bytes of INT4 codes (r[0]) become 32 bytes, a code in the low half of
-// each: code e of a word is the low nibble of byte e, e + 4 the high nibble.
-// `swap`: the second eight bytes come first.
-__device__ __forceinline__ void widen4(uint4 *r, bool swap) {
-  const uint4 x = swap ? make_uint4(r[0].z, r[0].w, r[0].x, r[0].y) : r[0];
-  const uint32_t m = 0x0f0f0f0fu;
-  r[0] = make_uint4(x.x & m, x.x >> 4 & m, x.y & m, x.y >> 4 & m);
-  r[1] = make_uint4(x.z & m, x.z >> 4 & m, x.w & m, x.w >> 4 & m);
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+// Sixteen codes from `from` (INT8: 16 bytes; INT4: 8 bytes, code e of a word the
+// low nibble of byte e, e + 4 the high nibble) to two neighbouring 16-byte
+// chunks `to`, `to` ^ 16.
+__device__ __forceinline__ void sixteen(const TreeCodec &f, bool int4, uint32_t from, uint32_t to) {
+  uint4 x;
+  if (int4) {
+    const uint2 y = lds64(from);
+    const uint32_t m = 0x0f0f0f0fu;
+    x = make_uint4(y.x & m, y.x >> 4 & m, y.y & m, y.y >> 4 & m);
+  } else {
+    x = lds128(from);
+  }
+  sts128(to, f.eight(x.x, x.y));
+  sts128(to ^ 16, f.eight(x.z, x.w));
 }
 
 __device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
 
-// Codes and rows are read once: no place in L1.
+// Rows are read once: no place in L1.
 __device__ __forceinline__ uint4 ldg16(const void *p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -223,226 +258,263 @@ __device__ __forceinline__ uint4 ldg16(const void *p) {
   return r;
 }
 
-// A thread of a producer group has a part of each of a tile's four units of 32
-// keys.  K: key tid / 4, channels 32 (tid % 4) and up.  Eight lanes are two
-// keys of four threads; threads 2 and 3 of a key take their chunks in the order
-// j ^ 2, which spreads the eight over the banks.
-struct TreeK {
-  uint32_t row, chan;  // key of the unit, first channel
-  uint32_t at[4];      // unit 0's place of chunk j (the j-th that the thread holds)
-  uint32_t swap;       // 0 or 2: the first chunk held
-
-  __device__ __forceinline__ TreeK(uint32_t st, int tid) {
-    row = tid >> 2;
-    chan = 32 * (tid & 3);
-    swap = tid & 2;
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      at[j] = st + ((tid >> 1) & 1) * kTreeSlab + row * 128 + (((4 * (tid & 1) + (j ^ swap)) ^ (row & 7)) << 4);
-  }
-  __device__ __forceinline__ void load(const uint8_t *pair, int half, bool int4, uint4 *r) const {
-    if (int4) {
-      r[0] = ldg16(pair + (32 * half + row) * 64 + chan / 2);
-      r[1] = make_uint4(0, 0, 0, 0);
-    } else {
-      const uint8_t *p = pair + (32 * half + row) * 128 + chan;
-      r[0] = ldg16(p + 8 * swap);
-      r[1] = ldg16(p + 16 - 8 * swap);
-    }
-  }
-  __device__ __forceinline__ void store(int u, bool int4, uint4 *r) const {
-    if (int4) widen4(r, swap);
-    const TreeCodec f(int4);
-    sts128(at[0] + 4096 * u, f.eight(r[0].x, r[0].y));
-    sts128(at[1] + 4096 * u, f.eight(r[0].z, r[0].w));
-    sts128(at[2] + 4096 * u, f.eight(r[1].x, r[1].y));
-    sts128(at[3] + 4096 * u, f.eight(r[1].z, r[1].w));
-  }
-  __device__ __forceinline__ void load_row(const __half *k, uint4 *r) const {
-#pragma unroll
-    for (int j = 0; j < 4; j++) r[j] = ldg16(k + chan + 8 * (j ^ swap));
-  }
-  __device__ __forceinline__ void store_row(int u, const uint4 *r) const {
-#pragma unroll
-    for (int j = 0; j < 4; j++) sts128(at[j] + 4096 * u, r[j]);
-  }
-};
-
-// V of INT8 / INT4 units: channel tid, all 32 keys of the unit.  Its two
-// 16-slot chunks are one aligned pair, swapped where the swizzle's lowest bit
-// is set: the halves are loaded in the order of the slots.  Eight lanes are
-// eight rows, all banks.
-struct TreeV {
-  uint32_t chan;
-  uint32_t at[4];  // unit 0's place of chunk j; odd units: ^ 64
-
-  __device__ __forceinline__ TreeV(uint32_t st, int tid) {
-    chan = tid;
-#pragma unroll
-    for (int j = 0; j < 4; j++) at[j] = st + chan * 128 + ((j ^ (chan & 7)) << 4);
-  }
-  __device__ __forceinline__ void load(const uint8_t *pair, int half, bool int4, uint4 *r) const {
-    if (int4) {
-      r[0] = ldg16(pair + kTileBytes + chan * 32 + 8 * ((2 * half) ^ ((chan >> 2) & 2)));
-      r[1] = make_uint4(0, 0, 0, 0);
-    } else {
-      const uint32_t x = (chan >> 1) & 3;
-      const uint8_t *p = pair + kTileBytes + chan * 64 + 16 * ((2 * half) ^ (x & 2));
-      r[0] = ldg16(p + 16 * (x & 1));
-      r[1] = ldg16(p + 16 - 16 * (x & 1));
-    }
-  }
-  __device__ __forceinline__ void store(int u, bool int4, uint4 *r) const {
-    if (int4) widen4(r, chan >> 2 & 1);
-    const TreeCodec f(int4);
-    const uint32_t odd = 64 * (u & 1), slab = (u >> 1) * kTreeSlab;
-    sts128((at[0] ^ odd) + slab, f.eight(r[0].x, r[0].y));
-    sts128((at[1] ^ odd) + slab, f.eight(r[0].z, r[0].w));
-    sts128((at[2] ^ odd) + slab, f.eight(r[1].x, r[1].y));
-    sts128((at[3] ^ odd) + slab, f.eight(r[1].z, r[1].w));
-  }
-};
-
-// FP16 V of one unit: the thread's two channels are two rows, its 16 keys two
-// chunks of each.  Lanes 4..7 of eight write their odd row first, so that the
-// eight rows differ modulo 8.
-__device__ __forceinline__ void store_v16(uint32_t st, int u, int tid, const uint32_t (&w)[16]) {
-  const int p = tid & 63, odd = (p >> 2) & 1;
-  const int c0 = 4 * (u & 1) + 2 * (tid >> 6);
-#pragma unroll
-  for (int s = 0; s < 2; s++) {
-    const int hi = s ^ odd, row = 2 * p + hi;
-    const uint32_t base = st + (u >> 1) * kTreeSlab + row * 128;
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        o[e] = __byte_perm(w[8 * j + 2 * e], w[8 * j + 2 * e + 1], hi ? 0x7632 : 0x5410);
-      sts128(base + (((c0 + j) ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-    }
-  }
-}
-
-// The K row (kv 1: V row) of key k of unit c of a tile of FP16 rows, or null.
-__device__ __forceinline__ const __half *tree_row(const TreeArgs &a, const TreeRec &r, int c, int k, int kv) {
-  if (r.flags & kTileCold)
-    return r.ok[c] >> k & 1 ? reinterpret_cast<const __half *>(r.at[c]) + (2 * k + kv) * kDim : nullptr;
-  const int i = r.row0 + 32 * c + k;
+// The K row (kv 1: V row) of row i of a tail tile (ring rows in the order of
+// their positions, then nodes), or null.
+__device__ __forceinline__ const __half *tail_row(const TreeArgs &a, const TreeRec &r, int i, int kv) {
+  i += r.row0;
   if (i < r.hot) return r.ring + (2 * ((r.cold + i) & (a.hot_tokens - 1)) + kv) * kDim;
   return i - r.hot < r.keys ? r.node[kv] + static_cast<size_t>(i - r.hot) * a.hkv * kDim : nullptr;
 }
 
-template <int MT, bool kF16>
-__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t k_s, uint32_t v_s, int n) {
-  const int tid = threadIdx.x & 127, lane = tid & 31, group = (threadIdx.x >> 7) & 1;
-  // a group's tiles have one stage of their own
-  static_assert(kTreeStages == kTreeGroups, "one stage per producer group");
-  const uint32_t vst = v_s + group * kTreeOperand;
-  const TreeK kp(k_s + group * kTreeOperand, tid);
-  const TreeV vp(vst, tid);
-  // the group's next tile: codes (K of unit c in 4 c, 4 c + 1, V in the next
-  // two) or K rows
-  uint4 x[16];
+// A tail tile: K, one half row (a slab's row) per thread; eight lanes are four
+// rows of two slabs, which begin four chunks apart.
+__device__ __forceinline__ void tail_k(const TreeArgs &a, const TreeRec &r, uint32_t kst, int tid) {
+  const int row = tid >> 1, half = tid & 1;
+  const __half *p = tail_row(a, r, row, 0);
+  uint4 x[8];
 #pragma unroll
-  for (int i = 0; i < 16; i++) x[i] = make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < 8; j++) x[j] = p ? ldg16(p + 64 * half + 8 * (j ^ (4 * half))) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    sts128(kst + half * kTreeSlab + row * 128 + ((j ^ (4 * half) ^ (row & 7)) << 4), x[j]);
+}
 
-  // one round per tile of the group, and one before the first that only loads
-  for (int j = group - kTreeGroups; j < n; j += kTreeGroups) {
-    if (j >= 0) {
-      const uint32_t ph = (j / kTreeStages) & 1;
-      TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-      const uint32_t flags = r.flags, fmt = r.fmt;
-      if (!tree_wait(sm, &sm.kempty[group], ph ^ 1, a)) return;
-      const bool rows = kF16 || !(flags & kTileCold);
-      if (rows) {
-        if (!(flags & kTileCold)) {
-          // ring rows and nodes, at most two of a unit's tiles
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            const __half *p = tree_row(a, r, c, kp.row, 0);
-            if (p) {
-              kp.load_row(p, x + 4 * c);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; i++) x[4 * c + i] = make_uint4(0, 0, 0, 0);
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; c++) kp.store_row(c, x + 4 * c);
-      } else if constexpr (!kF16) {
-#pragma unroll
-        for (int c = 0; c < 4; c++) kp.store(c, fmt >> c & 1, x + 4 * c);
-      }
-      warp_arrive(&sm.kfull[group], lane);
-      if (!rows && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
-      if (!tree_wait(sm, &sm.vempty[group], ph ^ 1, a)) return;
-      if (rows) {
-        const int k0 = 16 * (tid >> 6), c2 = 2 * (tid & 63);
+// V: two channels of a unit's keys per thread.  Lane k knows key k's row.
+// Lanes 4..7 of eight write their odd row first, so that the eight rows differ
+// modulo 8.
+__device__ __forceinline__ void tail_v(const TreeArgs &a, TreeRec &r, uint32_t vst, int tid) {
+  const int lane = tid & 31, u = tid >> 6, pair = tid & 63, odd = (pair >> 2) & 1;
+  const uint64_t mine = reinterpret_cast<uint64_t>(tail_row(a, r, 32 * u + lane, 1));
+  const int ring = r.hot - (r.row0 + 32 * u);  // ring rows of the unit
+  uint32_t bad = 0;
 #pragma unroll 1
-        for (int c = 0; c < 4; c++) {
-          // lane k knows key k's row; every thread takes two channels of 16 keys
-          const uint64_t mine = reinterpret_cast<uint64_t>(tree_row(a, r, c, lane, 1));
-          uint32_t w[16];
+  for (int h = 0; h < 2; h++) {
+    uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 16; k++) {
-            const uint64_t p = __shfl_sync(0xffffffffu, mine, k0 + k);
-            w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + c2)) : 0u;
-          }
-          if (!(flags & kTileCold)) {
-            // A node's V that is not finite must not meet the zero weight of a
-            // row that does not attend the node: it becomes 0 here and the
-            // record names the node; the rows that do attend it add it at the
-            // end
-            const int ring = r.hot - (r.row0 + 32 * c + k0);  // ring rows among the 16
-            uint32_t b = 0;
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-              uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
-              if (k < ring) nf = 0;
-              w[k] &= ~((nf >> 15) * 0xffffu);
-              b |= nf ? 1u << k : 0u;
-            }
-            b = __reduce_or_sync(0xffffffffu, b << k0);
-            if (lane == 0) r.bad[tid >> 5][c] = b;
-          }
-          store_v16(vst, c, tid, w);
-        }
-      } else if constexpr (!kF16) {
-#pragma unroll
-        for (int c = 0; c < 4; c++) vp.store(c, fmt >> c & 1, x + 4 * c + 2);
-      }
-      warp_arrive(&sm.vfull[group], lane);
-      if (rows && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+    for (int k = 0; k < 16; k++) {
+      const uint64_t p = __shfl_sync(0xffffffffu, mine, 16 * h + k);
+      w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + 2 * pair)) : 0u;
     }
-    // the group's next tile: it has the time of two tiles to come
-    const int next = j + kTreeGroups;
-    if (next >= n) break;
-    if (next % kTreeBatch < kTreeGroups) {
-      const int batch = next / kTreeBatch;
+    // A node's V that is not finite must not meet the zero weight of a row that
+    // does not attend the node: it becomes 0 here and the record names the
+    // node; the rows that do attend it add it at the end
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+      uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
+      if (16 * h + k < ring) nf = 0;
+      w[k] &= ~((nf >> 15) * 0xffffu);
+      bad |= nf ? 1u << (16 * h + k) : 0u;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; s++) {
+      const int hi = s ^ odd, row = 2 * pair + hi;
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          o[e] = __byte_perm(w[8 * j + 2 * e], w[8 * j + 2 * e + 1], hi ? 0x7632 : 0x5410);
+        sts128(vst + (u >> 1) * kTreeSlab + row * 128 + (((4 * (u & 1) + 2 * h + j) ^ (row & 7)) << 4),
+               make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 0) r.bad[tid >> 5] = bad;
+}
+
+template <int MT, bool kF16>
+__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t k_s, uint32_t v_s, uint32_t c_s,
+                                             int n) {
+  constexpr int kPieces = TreeSmem<MT>::kPieces;
+  const int tid = threadIdx.x & 255, lane = tid & 31;
+  // K: the thread's key of a unit and its 16 channels.  Eight lanes are
+  // channels 0..63 of one key and 64..127 of the next: all banks of both the
+  // piece and (as neighbouring rows of different slabs) the operand
+  const int hi = (tid >> 2) & 1, key = 2 * (tid >> 4) + hi, ch16 = (tid & 3) + 4 * (hi ^ ((tid >> 3) & 1));
+  const uint32_t k_to = (ch16 >> 2) * kTreeSlab + key * 128 + (((2 * (ch16 & 3)) ^ (key & 7)) << 4);
+  // V: channel (tid + 256 i) / 4 and 16-slot chunk position tid % 4 of a 64-token
+  // tile; eight lanes are two channels of four chunks
+  const int v_ch = tid >> 2, v_pos = tid & 3;
+  int at = 0;         // the next piece
+  uint32_t turn = 0;  // the ring's turn, modulo 2
+  auto piece_full = [&]() { return tree_wait(sm, &sm.cfull[at], turn, a); };
+  auto piece_done = [&]() {
+    warp_arrive(&sm.cempty[at], lane);
+    if (++at == kPieces) {
+      at = 0;
+      turn ^= 1;
+    }
+  };
+
+  for (int j = 0; j < n; j++) {
+    const int s = j & (kTreeStages - 1);
+    const uint32_t ph = (j / kTreeStages) & 1;
+    const uint32_t kst = k_s + s * kTreeOperand, vst = v_s + s * kTreeOperand;
+    if (j % kTreeBatch == 0) {
+      const int batch = j / kTreeBatch;
       if (!tree_wait(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) return;
     }
-    const TreeRec &r = sm.rec[next & (kTreeRecs - 1)];
-    if (r.flags & kTileCold) {
+    TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
+    const bool cold = r.flags & kTileCold;
+    if (!tree_wait(sm, &sm.kempty[s], ph ^ 1, a)) return;
+    if (!cold) {
+      tail_k(a, r, kst, tid);
+      warp_arrive(&sm.kfull[s], lane);
+      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
+      tail_v(a, r, vst, tid);
+      warp_arrive(&sm.vfull[s], lane);
+    } else if constexpr (kF16) {
+      // pieces of 16 rows of K and V
+      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
+#pragma unroll 1
+      for (int p = 0; p < 8; p++) {
+        if (!piece_full()) return;
+        const uint32_t c = c_s + at * kTreePiece;
+        {
+          const int row = tid >> 4, c16 = tid & 15, to = 16 * p + row;
+          sts128(kst + (c16 >> 3) * kTreeSlab + to * 128 + (((c16 & 7) ^ (to & 7)) << 4), lds128(c + row * 512 + c16 * 16));
+        }
+        const int pair = tid & 63, rows = 4 * (tid >> 6), odd = (pair >> 2) & 1;
+        const uint32_t ok = r.ok[p >> 1] >> (16 * (p & 1) + rows);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {  // (keys that are not there may hold anything)
+          w[k] = lds32(c + (rows + k) * 512 + 256 + 4 * pair);
+          if (!(ok >> k & 1)) w[k] = 0;
+        }
+        const int to = 16 * p + rows;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          const int up = q ^ odd, row = 2 * pair + up, sel = up ? 0x7632 : 0x5410;
+          sts64(vst + (to >> 6) * kTreeSlab + row * 128 + ((((to & 63) >> 3) ^ (row & 7)) << 4) + (to & 4) * 2,
+                __byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel));
+        }
+        piece_done();
+      }
+      warp_arrive(&sm.kfull[s], lane);
+      if (lane == 0) mbar_arrive(&sm.vfull[s]);
+    } else {
       const uint32_t fmt = r.fmt;
+#pragma unroll 1
+      for (int p = 0; p < 2; p++) {
+        if (!piece_full()) return;
+        const uint32_t c = c_s + at * kTreePiece;
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
-        const uint8_t *at = r.at[c];
-        if (!at) {  // a unit without keys: its logits are masked, its weights 0
+        for (int i = 0; i < 2; i++) {
+          const bool int4 = fmt >> (2 * p + i) & 1;
+          sixteen(TreeCodec(int4), int4, c + 4096 * i + (int4 ? key * 64 + ch16 * 8 : key * 128 + ch16 * 16),
+                  kst + k_to + 4096 * (2 * p + i));
+        }
+        piece_done();
+      }
+      warp_arrive(&sm.kfull[s], lane);
+      if (lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
+      // 32-token blocks: a piece per unit, whose slots 0..31 are its tokens
+      const bool small = a.bshift == 5;
+#pragma unroll 1
+      for (int p = 0; p < (small ? 4 : 2); p++) {
+        if (!piece_full()) return;
+        const uint32_t c = c_s + at * kTreePiece;
+        const bool int4 = fmt >> (small ? p : 2 * p) & 1;
+        const TreeCodec f(int4);
 #pragma unroll
-          for (int i = 0; i < 4; i++) x[4 * c + i] = make_uint4(0, 0, 0, 0);
-        } else if constexpr (kF16) {
-          kp.load_row(reinterpret_cast<const __half *>(at) + 2 * kp.row * kDim, x + 4 * c);
-        } else {
-          kp.load(at, fmt >> (4 + c) & 1, fmt >> c & 1, x + 4 * c);
-          vp.load(at, fmt >> (4 + c) & 1, fmt >> c & 1, x + 4 * c + 2);
+        for (int i = 0; i < 2; i++) {
+          const int ch = v_ch + 64 * i, chunk = v_pos ^ (ch >> (int4 ? 2 : 1) & 3);  // slots 16 chunk ..
+          const uint32_t from = c + (int4 ? ch * 32 + v_pos * 8 : ch * 64 + v_pos * 16);
+          const int to = small ? 4 * (p & 1) + 2 * chunk : 2 * chunk;
+          if (!small || chunk < 2)
+            sixteen(f, int4, from, vst + (small ? p >> 1 : p) * kTreeSlab + ch * 128 + ((to ^ (ch & 7)) << 4));
+        }
+        piece_done();
+      }
+      warp_arrive(&sm.vfull[s], lane);
+    }
+    if ((kF16 || !cold) && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+  }
+}
+
+// ---- the copy warp ----
+
+// (bulk_g2s of common.cuh with the shared address as a number)
+__device__ __forceinline__ void bulk_to(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
+// One thread brings the bytes of the cold tiles: per tile K of units 0, 1 and 2,
+// 3 (4096 bytes apart), then their V tiles (32-token blocks: one per unit); FP16
+// rows 16 at a time.
+template <int MT, bool kF16>
+__device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t c_s, int n) {
+  constexpr int kPieces = TreeSmem<MT>::kPieces;
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = l2_policy_evict_first();
+  const bool small = a.bshift == 5;
+  int at = 0, sent = 0;
+  uint32_t turn = 0;
+  bool ok = true;
+  for (int j = 0; j < n && ok; j++) {
+    if (j % kTreeBatch == 0) {
+      const int batch = j / kTreeBatch;
+      if (!tree_wait(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
+    }
+    const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
+    if (!(r.flags & kTileCold)) continue;
+    const int pieces = kF16 ? 8 : small ? 6 : 4;
+    const uint32_t fmt = r.fmt;
+#pragma unroll 1
+    for (int p = 0; p < pieces; p++) {
+      ok = tree_wait(sm, &sm.cempty[at], turn ^ 1, a);
+      if (!ok) break;
+      // the piece: up to two parts {source, bytes, place}
+      const uint8_t *src[2] = {nullptr, nullptr};
+      uint32_t bytes[2] = {0, 0};
+      if (kF16) {
+        if (r.at[p >> 1]) {
+          src[0] = r.at[p >> 1] + (p & 1) * kTreePiece;
+          bytes[0] = kTreePiece;
+        }
+      } else if (p < 2) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int u = 2 * p + i;
+          if (r.at[u]) {
+            bytes[i] = fmt >> u & 1 ? 2048 : 4096;
+            src[i] = r.at[u] + (fmt >> (4 + u) & 1 ? bytes[i] : 0);
+          }
+        }
+      } else {
+        const int u = small ? p - 2 : 2 * (p - 2);
+        if (r.at[u]) {
+          src[0] = r.at[u] + kTileBytes;
+          bytes[0] = fmt >> u & 1 ? kTileBytes / 2 : kTileBytes;
         }
       }
-    } else {  // (nothing of the last tile lives on)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.cfull[at], bytes[0] + bytes[1]);
 #pragma unroll
-      for (int i = 0; i < 16; i++) x[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 2; i++)
+          if (bytes[i]) bulk_to(c_s + at * kTreePiece + 4096 * i, src[i], bytes[i], &sm.cfull[at], policy);
+      }
+      __syncwarp();
+      sent++;
+      if (++at == kPieces) {
+        at = 0;
+        turn ^= 1;
+      }
     }
+  }
+  // the copies in flight land before the CTA ends, also when nobody takes them
+  for (int i = 0; i < kPieces && i < sent; i++) {
+    if (--at < 0) {
+      at = kPieces - 1;
+      turn ^= 1;
+    }
+    mbar_wait_bounded(&sm.cfull[at], turn, kDefaultWaitCycles);
   }
 }
 
@@ -461,7 +533,7 @@ __device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg
                                         int lane) {
   const int G = a.group, n = min(128 * MT, rows - mg * 128 * MT), c = lane & 15;
   const __half *q = a.q + (static_cast<size_t>(b) * a.max_tree * a.hq + hk * G) * kDim + 8 * c;
-  const uint32_t to = st + (c >> 3) * kTreeSlab;
+  const uint32_t slab = MT == 1 ? a.q_rows * 128 : kTreeSlab, to = st + (c >> 3) * slab;
 #pragma unroll 2
   for (int r = lane >> 4; r < n; r += 2) {
     const int row = mg * 128 * MT + r, t = row_node(a, row);
@@ -476,7 +548,6 @@ __device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg
 // Lane 4 k + c looks up unit c of tile k of a batch.
 template <int MT, bool kF16>
 __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, int n) {
-  constexpr int kQ = TreeSmem<MT>::kQ;
   const int lane = threadIdx.x & 31, k = (lane >> 2) & (kTreeBatch - 1), c = lane & 3;
   const bool on = lane < 4 * kTreeBatch;
   int b = sm.start_b, segs = 0;     // segments begun before the batch
@@ -584,7 +655,7 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
     // the segments that begin in this batch: their query rows
     for (uint32_t f = firsts; f; f &= f - 1, segs++) {
       const int s = segs;
-      const int from = __ffs(f) - 1, i = s % kQ;
+      const int from = __ffs(f) - 1, i = a.q_bufs == 2 ? s & 1 : 0;
       const int fb = __shfl_sync(0xffffffffu, b, from), fhk = __shfl_sync(0xffffffffu, hk, from);
       const int fmg = __shfl_sync(0xffffffffu, mg, from), frows = __shfl_sync(0xffffffffu, rows, from);
       const int fleft = __shfl_sync(0xffffffffu, left, from), fj = __shfl_sync(0xffffffffu, j, from);
@@ -600,7 +671,7 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
           q_use |= 1u << at;
           q_count = (q_count & ~(255u << (8 * at))) | (((q_count >> (8 * at)) + 1) & 255u) << (8 * at);
         }
-      fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * MT * kTreeOperand, &sm.qfull[i], lane);
+      fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * 256 * a.q_rows, &sm.qfull[i], lane);
     }
     pos += kTreeBatch;
   }
@@ -613,7 +684,6 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
 template <int MT>
 __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
                                          uint32_t tmem, int n, int i) {
-  constexpr int kQ = TreeSmem<MT>::kQ;
   constexpr uint32_t idesc = tc_idesc_f16(128);
   const uint32_t t_s = tmem + 128 * i, t_p = t_s + 64, t_o = tmem + 256 + 128 * i;
   int used = 0, begun = 0;  // tiles and segments of the stream
@@ -623,24 +693,26 @@ __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, ui
     // S = Q K^T (it replaces the weights of the stream's last P V)
     if (!tree_wait(sm, &sm.kfull[s], ph, a)) return;
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-    const uint32_t flags = r.flags, seg = flags >> kTileSegShift;
+    const uint32_t flags = r.flags, seg = flags >> kTileSegShift & 3;
+    const int qb = a.q_bufs == 2 ? seg & 1 : 0;  // the segment's Q buffer
     const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
     const bool last = MT == 1 ? r.left < 2 : flags & kTileLast;
-    if (first && !tree_wait(sm, &sm.qfull[seg % kQ], (seg / kQ) & 1, a)) return;
+    if (first && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return;
     fence_proxy_async_smem();
     tc_fence_after();
     {
-      const uint64_t dq = tc_desc_sw128(q_s + ((seg % kQ) * MT + (MT == 2 ? i : 0)) * kTreeOperand);
+      const uint64_t dq = tc_desc_sw128(q_s + (MT == 2 ? i * kTreeOperand : qb * 256 * a.q_rows));
+      const uint32_t q_slab = MT == 1 ? a.q_rows * 8 : kTreeSlab >> 4;
       const uint64_t dk = tc_desc_sw128(k_s + s * kTreeOperand);
       if (tc_elect()) {
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-          const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
-          tc_mma_ss(t_s, dq + o, dk + o, idesc, k > 0);
+          const uint32_t o = 2 * (k & 3);
+          tc_mma_ss(t_s, dq + (k >> 2) * q_slab + o, dk + (k >> 2) * (kTreeSlab >> 4) + o, idesc, k > 0);
         }
         tc_commit(&sm.sfull[i]);
         tc_commit(&sm.kempty[s]);
-        if (last) tc_commit(&sm.qempty[seg % kQ][i]);
+        if (last) tc_commit(&sm.qempty[qb][i]);
       }
       __syncwarp();
     }
@@ -716,9 +788,7 @@ __device__ __forceinline__ uint32_t tree_nodes(const TreeRec &r, int c, int k, u
   uint32_t own = 0, bad = 0;
   if (k >= 0) own = k < 64 ? static_cast<uint32_t>(nodes >> k) : 0u;
   else if (k > -32) own = static_cast<uint32_t>(nodes << -k);
-#pragma unroll
-  for (int w = 0; w < 4; w++) bad |= r.bad[w][c];
-  bad &= own;
+  bad = (r.bad[2 * c] | r.bad[2 * c + 1]) & own;
   if (bad) odd |= k >= 0 ? static_cast<uint64_t>(bad) << k : static_cast<uint64_t>(bad) >> -k;
   return own;
 }
@@ -858,13 +928,14 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
       for (int h = 1; h >= 0; h--) {
-        uint32_t v[64], p[32];
+        uint32_t v[64];
         tc_ld64(t_s + 64 * h, v);
         tc_wait_ld(v);
 #pragma unroll
         for (int u = 0; u < 2; u++) {
           const float s = plain ? r.k_scale[2 * h + u] * a.qk_scale : 1.f, f = r.v_scale[2 * h + u] * inv;
           const uint64_t s2 = pack2(s, s), f2 = pack2(f, f);
+          uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             float x, y;
@@ -873,10 +944,10 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
             if (k & 2) sum1 = add2(sum1, e);
             else sum0 = add2(sum0, e);
             unpack2(mul2(e, f2), x, y);
-            p[16 * u + (k >> 1)] = half2_bits(x, y);
+            p[k >> 1] = half2_bits(x, y);
           }
+          tc_st16(t_p + 32 * h + 16 * u, p);
         }
-        tc_st32(t_p + 32 * h, p);
       }
       float x, y;
       unpack2(add2(sum0, sum1), x, y);
@@ -975,9 +1046,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   using Shape = TreeShape<MT>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, k_s = q_s + Shape::kQBytes, v_s = k_s + kTreeStages * kTreeOperand;
-  TreeSmem<MT> &sm = *reinterpret_cast<TreeSmem<MT> *>(raw + (base - smem_addr(raw)) + Shape::kQBytes +
-                                                       2 * kTreeStages * kTreeOperand);
+  const uint32_t q_s = base, k_s = q_s + Shape::kQBytes, v_s = k_s + kTreeStages * kTreeOperand, c_s = base + Shape::kTiles;
+  TreeSmem<MT> &sm = *reinterpret_cast<TreeSmem<MT> *>(raw + (base - smem_addr(raw)) + Shape::kTiles +
+                                                       TreeSmem<MT>::kPieces * kTreePiece);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
   constexpr int kMmaWarp = kTreeSoft + kTreeProd, kScoutWarp = kMmaWarp + kTreeMma;
@@ -1003,8 +1074,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     a.shared_units[blockIdx.x] = make_int4(0, 0, 0, 0);
     sm.abort = 0;
     for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.kfull[i], kTreeProd / kTreeGroups);
-      mbar_init(&sm.vfull[i], kTreeProd / kTreeGroups);
+      mbar_init(&sm.kfull[i], kTreeProd);
+      mbar_init(&sm.vfull[i], kTreeProd);
       mbar_init(&sm.kempty[i], MT);
       mbar_init(&sm.vempty[i], MT);
       mbar_init(&sm.rfull[i], 1);
@@ -1015,11 +1086,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       mbar_init(&sm.ofree[i], 8);
       mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd / kTreeGroups);
-    for (int i = 0; i < TreeSmem<MT>::kQ; i++) {
+    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd);
+    for (int i = 0; i < 2; i++) {
       mbar_init(&sm.qfull[i], 32);
       mbar_init(&sm.qempty[i][0], 1);
       mbar_init(&sm.qempty[i][1], 1);
+    }
+    for (int i = 0; i < TreeSmem<MT>::kPieces; i++) {
+      mbar_init(&sm.cfull[i], 1);
+      mbar_init(&sm.cempty[i], kTreeProd);
     }
     mbar_init(&sm.xfull, 8);
     mbar_fence_init();
@@ -1057,9 +1132,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   const uint32_t tmem = sm.tmem;
 
   if (warp < kTreeSoft) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftRegs));
     tree_softmax<MT>(a, sm, tmem, n_tiles);
   } else if (warp < kMmaWarp) {
-    tree_produce<MT, kF16>(a, sm, k_s, v_s, n_tiles);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeProdRegs));
+    tree_produce<MT, kF16>(a, sm, k_s, v_s, c_s, n_tiles);
   } else if (warp < kScoutWarp) {
     const int i = warp - kMmaWarp;
     tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
@@ -1069,6 +1146,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     __syncwarp();
     if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);
     __syncwarp();
+  } else if (warp > kScoutWarp) {
+    tree_copy<MT, kF16>(a, sm, c_s, n_tiles);
   } else {
     tree_scout<MT, kF16>(a, sm, q_s, n_tiles);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1145,6 +1224,12 @@ static cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(tree_kernel<MT, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Shape::kBytes));
     if (e != cudaSuccess) return e;
+    // the softmax warps' registers come from the producers', of what the launch
+    // really has
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, tree_kernel<MT, kF16>);
+    if (e != cudaSuccess) return e;
+    if (2 * at.numRegs < kTreeSoftRegs + kTreeProdRegs) return cudaErrorInvalidKernelImage;
     if (dev < 31) configured_dev_mask |= 1 << dev;
   }
   tree_kernel<MT, kF16><<<a.ctas, kTreeThreads, Shape::kBytes, stream>>>(a);

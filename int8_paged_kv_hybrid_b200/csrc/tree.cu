@@ -25,8 +25,9 @@
 // Inside a CTA (20 warps): a scout warp looks the tiles up (block table, scales,
 // segment ends) some tiles ahead, writes their records, starts their way into
 // L2 and fetches the query rows; a copy warp brings their bytes into a ring in
-// shared memory by bulk copies; eight producer warps turn codes or rows into
-// FP16 in the 128-byte swizzled layout of the MMA's shared operands; two groups
+// shared memory by bulk copies; four producer warps turn K, four V, from codes
+// or rows into FP16 in the 128-byte swizzled layout of the MMA's shared
+// operands; two groups
 // of four softmax warps (one query row per thread) keep two softmax streams and
 // write the weights over the logits in TMEM, where the second product reads
 // them as its A operand; a warp for each stream issues its MMAs.  The streams
@@ -46,7 +47,7 @@ constexpr int kTreeBatch = 4;                // tiles the scout looks up at once
 constexpr int kTreeRecs = 2 * kTreeBatch;    // tile records
 constexpr uint32_t kTreeOperand = 128 * 256; // bytes of a 128 x 128 FP16 operand
 constexpr uint32_t kTreeSlab = kTreeOperand / 2;  // its halves of 64 columns
-constexpr uint32_t kTreePiece = 8192;        // a piece of the ring of codes or rows
+constexpr uint32_t kPiece = 8192;            // of the rings of codes or rows
 constexpr float kLagLog2 = 6.f;
 constexpr float kLagScale = 256.f;
 
@@ -70,7 +71,7 @@ struct TreeRec {
   float k_scale[4];      // 1 for FP16 rows
   float v_scale[4];
   uint32_t ok[4];        // keys that every row attends
-  uint32_t bad[8];       // keys of unit i / 2 of a tail tile with a V that is not finite (by producer warp i)
+  uint32_t bad[4][4];    // [V warp][unit]: keys of a tail tile with a V that is not finite (by the producers)
   uint32_t fmt;          // bit c: unit c is INT4; bit 4 + c: it is the second half of its slots
   uint32_t flags;
   float v_max;           // largest |v_scale|
@@ -92,14 +93,16 @@ struct TreeStat {
 
 template <int MT>
 struct TreeSmem {
-  static constexpr int kPieces = MT == 1 ? 6 : 3;
+  // pieces of 8192 bytes: a ring of codes of K and one of V, or one of FP16 rows
+  static constexpr int kPieces = MT == 1 ? 6 : 4;
   // MMA operands: MT 1 stage and stream are one; MT 2 both streams free a stage
   uint64_t kfull[kTreeStages], kempty[kTreeStages], vfull[kTreeStages], vempty[kTreeStages];
   uint64_t cfull[kPieces], cempty[kPieces];
   uint64_t rfull[2], rfree[2];     // records, by batch parity
   uint64_t mfull[kTreeRecs];       // a record's tile is in shared memory
-  uint64_t qfull[2];
-  uint64_t qempty[2][2];           // by stream
+  // Q by buffer and stream: a stream sits out segments of one tile, and must
+  // not miss a phase of its barriers
+  uint64_t qfull[2][2], qempty[2][2];
   uint64_t sfull[2], pfull[2], odone[2], ofree[2];  // by stream
   uint64_t xfull;                  // MT 1: both streams' rows are in `stat`
   uint64_t drain[2];
@@ -119,7 +122,8 @@ template <int MT>
 struct TreeShape {
   static constexpr uint32_t kQBytes = MT * kTreeOperand;
   static constexpr uint32_t kTiles = kQBytes + 2 * kTreeStages * kTreeOperand;
-  static constexpr uint32_t kBytes = 1024 + kTiles + TreeSmem<MT>::kPieces * kTreePiece + sizeof(TreeSmem<MT>);
+  static constexpr uint32_t kBytes = kTiles + TreeSmem<MT>::kPieces * kPiece + sizeof(TreeSmem<MT>);
+  static_assert(kBytes <= 232448, "shared memory of an SM");
 };
 
 // ---- the list of tiles ----
@@ -150,26 +154,35 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   return s;
 }
 
-// Wait for phase `parity`; false (in all lanes) when the wait or the kernel
-// gave up.  Called by whole warps.
+// Wait for phase `parity`; false when the wait or the kernel gave up.
+template <typename Sm>
+__device__ __forceinline__ bool tree_wait_slow(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
+  const bool quick = a.wait_cycles < kShortWaitCycles;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  while (!(quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
+    if (sm.abort) return false;
+    if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
+      sm.abort = 1;
+      set_status(a.status, HYB_STATUS_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// ... by one thread,
+template <typename Sm>
+__device__ __forceinline__ bool tree_wait_one(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
+  return mbar_test_wait(bar, parity) || tree_wait_slow(sm, bar, parity, a);
+}
+
+// ... and by a whole warp, with one answer.
 template <typename Sm>
 __device__ __forceinline__ bool tree_wait(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  const bool quick = a.wait_cycles < kShortWaitCycles;
-  bool ok = quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const uint32_t t0 = static_cast<uint32_t>(clock());
-    while (!ok) {
-      ok = quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-      if (ok || sm.abort) break;
-      if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
-        sm.abort = 1;
-        set_status(a.status, HYB_STATUS_TIMEOUT);
-        break;
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  return ok;
+  bool ok = mbar_test_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (!ok) ok = tree_wait_slow(sm, bar, parity, a);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // The node of a query row: row / (Hq / Hkv), by a multiplication that is exact
@@ -231,23 +244,18 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
-// Sixteen codes from `from` (INT8: 16 bytes; INT4: 8 bytes, code e of a word the
-// low nibble of byte e, e + 4 the high nibble) to two neighbouring 16-byte
-// chunks `to`, `to` ^ 16.
-__device__ __forceinline__ void sixteen(const TreeCodec &f, bool int4, uint32_t from, uint32_t to) {
-  uint4 x;
-  if (int4) {
-    const uint2 y = lds64(from);
-    const uint32_t m = 0x0f0f0f0fu;
-    x = make_uint4(y.x & m, y.x >> 4 & m, y.y & m, y.y >> 4 & m);
-  } else {
-    x = lds128(from);
-  }
+// Sixteen codes, INT8 or (of eight bytes, code e of a word the low nibble of byte
+// e, e + 4 the high nibble) INT4, to two neighbouring 16-byte chunks `to`, `to` ^ 16.
+__device__ __forceinline__ void put16(const TreeCodec &f, uint4 x, uint32_t to) {
   sts128(to, f.eight(x.x, x.y));
   sts128(to ^ 16, f.eight(x.z, x.w));
 }
-
-__device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
+__device__ __forceinline__ uint4 get16(bool int4, uint32_t from) {
+  if (!int4) return lds128(from);
+  const uint2 y = lds64(from);
+  const uint32_t m = 0x0f0f0f0fu;
+  return make_uint4(y.x & m, y.x >> 4 & m, y.y & m, y.y >> 4 & m);
+}
 
 // Rows are read once: no place in L1.
 __device__ __forceinline__ uint4 ldg16(const void *p) {
@@ -258,6 +266,8 @@ __device__ __forceinline__ uint4 ldg16(const void *p) {
   return r;
 }
 
+__device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
+
 // The K row (kv 1: V row) of row i of a tail tile (ring rows in the order of
 // their positions, then nodes), or null.
 __device__ __forceinline__ const __half *tail_row(const TreeArgs &a, const TreeRec &r, int i, int kv) {
@@ -266,172 +276,195 @@ __device__ __forceinline__ const __half *tail_row(const TreeArgs &a, const TreeR
   return i - r.hot < r.keys ? r.node[kv] + static_cast<size_t>(i - r.hot) * a.hkv * kDim : nullptr;
 }
 
-// A tail tile: K, one half row (a slab's row) per thread; eight lanes are four
-// rows of two slabs, which begin four chunks apart.
+// A tail tile's K: one row per thread; eight lanes are eight rows.
 __device__ __forceinline__ void tail_k(const TreeArgs &a, const TreeRec &r, uint32_t kst, int tid) {
-  const int row = tid >> 1, half = tid & 1;
-  const __half *p = tail_row(a, r, row, 0);
-  uint4 x[8];
+  const __half *p = tail_row(a, r, tid, 0);
+#pragma unroll 1
+  for (int half = 0; half < 2; half++) {
+    uint4 x[8];
 #pragma unroll
-  for (int j = 0; j < 8; j++) x[j] = p ? ldg16(p + 64 * half + 8 * (j ^ (4 * half))) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 8; j++) x[j] = p ? ldg16(p + 64 * half + 8 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int j = 0; j < 8; j++)
-    sts128(kst + half * kTreeSlab + row * 128 + ((j ^ (4 * half) ^ (row & 7)) << 4), x[j]);
+    for (int j = 0; j < 8; j++) sts128(kst + half * kTreeSlab + tid * 128 + ((j ^ (tid & 7)) << 4), x[j]);
+  }
 }
 
-// V: two channels of a unit's keys per thread.  Lane k knows key k's row.
-// Lanes 4..7 of eight write their odd row first, so that the eight rows differ
-// modulo 8.
+// Two channels (2 pair, + 1) of eight keys (words w) to a chunk of the channels'
+// rows.  Lanes 4..7 of eight write their odd row first, so that the eight rows
+// differ modulo 8.
+__device__ __forceinline__ void put_v(uint32_t vst, int pair, int key, const uint32_t *w) {
+  const int odd = (pair >> 2) & 1;
+#pragma unroll
+  for (int s = 0; s < 2; s++) {
+    const int hi = s ^ odd, row = 2 * pair + hi, sel = hi ? 0x7632 : 0x5410;
+    sts128(vst + (key >> 6) * kTreeSlab + row * 128 + (((key >> 3 & 7) ^ (row & 7)) << 4),
+           make_uint4(__byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel), __byte_perm(w[4], w[5], sel),
+                      __byte_perm(w[6], w[7], sel)));
+  }
+}
+
+// A tail tile's V: two channels of 16 of every unit's keys per thread.  Lane k
+// knows key k's row.
 __device__ __forceinline__ void tail_v(const TreeArgs &a, TreeRec &r, uint32_t vst, int tid) {
-  const int lane = tid & 31, u = tid >> 6, pair = tid & 63, odd = (pair >> 2) & 1;
-  const uint64_t mine = reinterpret_cast<uint64_t>(tail_row(a, r, 32 * u + lane, 1));
-  const int ring = r.hot - (r.row0 + 32 * u);  // ring rows of the unit
-  uint32_t bad = 0;
+  const int lane = tid & 31, k0 = 16 * (tid >> 6), pair = tid & 63;
 #pragma unroll 1
-  for (int h = 0; h < 2; h++) {
+  for (int u = 0; u < 4; u++) {
+    const uint64_t mine = reinterpret_cast<uint64_t>(tail_row(a, r, 32 * u + lane, 1));
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; k++) {
-      const uint64_t p = __shfl_sync(0xffffffffu, mine, 16 * h + k);
+      const uint64_t p = __shfl_sync(0xffffffffu, mine, k0 + k);
       w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + 2 * pair)) : 0u;
     }
     // A node's V that is not finite must not meet the zero weight of a row that
     // does not attend the node: it becomes 0 here and the record names the
     // node; the rows that do attend it add it at the end
+    const int ring = r.hot - (r.row0 + 32 * u + k0);  // ring rows among the 16
+    uint32_t bad = 0;
 #pragma unroll
     for (int k = 0; k < 16; k++) {
       uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
-      if (16 * h + k < ring) nf = 0;
+      if (k < ring) nf = 0;
       w[k] &= ~((nf >> 15) * 0xffffu);
-      bad |= nf ? 1u << (16 * h + k) : 0u;
+      bad |= nf ? 1u << k : 0u;
     }
-#pragma unroll
-    for (int s = 0; s < 2; s++) {
-      const int hi = s ^ odd, row = 2 * pair + hi;
-#pragma unroll
-      for (int j = 0; j < 2; j++) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-          o[e] = __byte_perm(w[8 * j + 2 * e], w[8 * j + 2 * e + 1], hi ? 0x7632 : 0x5410);
-        sts128(vst + (u >> 1) * kTreeSlab + row * 128 + (((4 * (u & 1) + 2 * h + j) ^ (row & 7)) << 4),
-               make_uint4(o[0], o[1], o[2], o[3]));
-      }
-    }
+    bad = __reduce_or_sync(0xffffffffu, bad << k0);
+    if (lane == 0) r.bad[tid >> 5][u] = bad;
+    put_v(vst, pair, 32 * u + k0, w);
+    put_v(vst, pair, 32 * u + k0 + 8, w + 8);
   }
-  bad = __reduce_or_sync(0xffffffffu, bad);
-  if (lane == 0) r.bad[tid >> 5] = bad;
 }
 
-template <int MT, bool kF16>
-__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t k_s, uint32_t v_s, uint32_t c_s,
-                                             int n) {
-  constexpr int kPieces = TreeSmem<MT>::kPieces;
-  const int tid = threadIdx.x & 255, lane = tid & 31;
-  // K: the thread's key of a unit and its 16 channels.  Eight lanes are
-  // channels 0..63 of one key and 64..127 of the next: all banks of both the
-  // piece and (as neighbouring rows of different slabs) the operand
-  const int hi = (tid >> 2) & 1, key = 2 * (tid >> 4) + hi, ch16 = (tid & 3) + 4 * (hi ^ ((tid >> 3) & 1));
-  const uint32_t k_to = (ch16 >> 2) * kTreeSlab + key * 128 + (((2 * (ch16 & 3)) ^ (key & 7)) << 4);
-  // V: channel (tid + 256 i) / 4 and 16-slot chunk position tid % 4 of a 64-token
-  // tile; eight lanes are two channels of four chunks
-  const int v_ch = tid >> 2, v_pos = tid & 3;
-  int at = 0;         // the next piece
-  uint32_t turn = 0;  // the ring's turn, modulo 2
+template <int MT, bool kF16, bool kV>
+__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t st, uint32_t c_s, int n) {
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  uint64_t *full = kV ? sm.vfull : sm.kfull, *empty = kV ? sm.vempty : sm.kempty;
+  const bool small = a.bshift == 5;
+  // the pieces: of FP16 rows both groups take all, of codes each its ring's
+  constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2, kFirst = !kF16 && kV ? kRing : 0;
+  int at = kFirst;
+  uint32_t turn = 0;  // modulo 2
   auto piece_full = [&]() { return tree_wait(sm, &sm.cfull[at], turn, a); };
   auto piece_done = [&]() {
     warp_arrive(&sm.cempty[at], lane);
-    if (++at == kPieces) {
-      at = 0;
+    if (++at == kFirst + kRing) {
+      at = kFirst;
       turn ^= 1;
     }
   };
+  // K: the thread's keys (8 i and this one of a unit) and its 16 channels.
+  // Eight lanes are channels 0..63 of one key and 64..127 of the next: all
+  // banks of both the piece and (as neighbouring rows of different slabs) the
+  // operand
+  const int hi = (tid >> 2) & 1, key = 2 * (tid >> 4) + hi, ch16 = (tid & 3) + 4 * (hi ^ ((tid >> 3) & 1));
+  const uint32_t k_to = (ch16 >> 2) * kTreeSlab + key * 128 + (((2 * (ch16 & 3)) ^ (key & 7)) << 4);
+  // V: channel tid / 4 and 32, 64, 96 more, 16-slot chunk position tid % 4 of a
+  // 64-token tile; eight lanes are two channels of four chunks
+  const int v_ch = tid >> 2, v_pos = tid & 3;
 
   for (int j = 0; j < n; j++) {
     const int s = j & (kTreeStages - 1);
-    const uint32_t ph = (j / kTreeStages) & 1;
-    const uint32_t kst = k_s + s * kTreeOperand, vst = v_s + s * kTreeOperand;
+    const uint32_t ph = (j / kTreeStages) & 1, to = st + s * kTreeOperand;
     if (j % kTreeBatch == 0) {
       const int batch = j / kTreeBatch;
       if (!tree_wait(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) return;
     }
     TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
     const bool cold = r.flags & kTileCold;
-    if (!tree_wait(sm, &sm.kempty[s], ph ^ 1, a)) return;
+    const uint32_t fmt = r.fmt;
+    if (!tree_wait(sm, &empty[s], ph ^ 1, a)) return;
     if (!cold) {
-      tail_k(a, r, kst, tid);
-      warp_arrive(&sm.kfull[s], lane);
-      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
-      tail_v(a, r, vst, tid);
-      warp_arrive(&sm.vfull[s], lane);
+      if constexpr (kV) tail_v(a, r, to, tid);
+      else tail_k(a, r, to, tid);
     } else if constexpr (kF16) {
       // pieces of 16 rows of K and V
-      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
 #pragma unroll 1
       for (int p = 0; p < 8; p++) {
         if (!piece_full()) return;
-        const uint32_t c = c_s + at * kTreePiece;
-        {
-          const int row = tid >> 4, c16 = tid & 15, to = 16 * p + row;
-          sts128(kst + (c16 >> 3) * kTreeSlab + to * 128 + (((c16 & 7) ^ (to & 7)) << 4), lds128(c + row * 512 + c16 * 16));
-        }
-        const int pair = tid & 63, rows = 4 * (tid >> 6), odd = (pair >> 2) & 1;
-        const uint32_t ok = r.ok[p >> 1] >> (16 * (p & 1) + rows);
-        uint32_t w[4];
+        const uint32_t c = c_s + at * kPiece;
+        if constexpr (kV) {
+          const int pair = tid & 63, rows = 8 * (tid >> 6);
+          const uint32_t ok = r.ok[p >> 1] >> (16 * (p & 1) + rows);
+          uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {  // (keys that are not there may hold anything)
-          w[k] = lds32(c + (rows + k) * 512 + 256 + 4 * pair);
-          if (!(ok >> k & 1)) w[k] = 0;
-        }
-        const int to = 16 * p + rows;
+          for (int k = 0; k < 8; k++) w[k] = lds32(c + (rows + k) * 512 + 256 + 4 * pair);
 #pragma unroll
-        for (int q = 0; q < 2; q++) {
-          const int up = q ^ odd, row = 2 * pair + up, sel = up ? 0x7632 : 0x5410;
-          sts64(vst + (to >> 6) * kTreeSlab + row * 128 + ((((to & 63) >> 3) ^ (row & 7)) << 4) + (to & 4) * 2,
-                __byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel));
+          for (int k = 0; k < 8; k++)  // (keys that are not there may hold anything)
+            if (!(ok >> k & 1)) w[k] = 0;
+          put_v(to, pair, 16 * p + rows, w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            const int row = (tid >> 4) + 8 * i, c16 = tid & 15;
+            sts128(to + (c16 >> 3) * kTreeSlab + (16 * p + row) * 128 + (((c16 & 7) ^ (row & 7)) << 4),
+                   lds128(c + row * 512 + c16 * 16));
+          }
         }
         piece_done();
       }
-      warp_arrive(&sm.kfull[s], lane);
-      if (lane == 0) mbar_arrive(&sm.vfull[s]);
-    } else {
-      const uint32_t fmt = r.fmt;
+    } else if constexpr (!kV) {
+      // two pieces of two units
 #pragma unroll 1
       for (int p = 0; p < 2; p++) {
         if (!piece_full()) return;
-        const uint32_t c = c_s + at * kTreePiece;
+        const uint32_t c = c_s + at * kPiece;
+        if ((fmt & 15) == 0) {
+          const TreeCodec f(false);
+          uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const bool int4 = fmt >> (2 * p + i) & 1;
-          sixteen(TreeCodec(int4), int4, c + 4096 * i + (int4 ? key * 64 + ch16 * 8 : key * 128 + ch16 * 16),
-                  kst + k_to + 4096 * (2 * p + i));
-        }
-        piece_done();
-      }
-      warp_arrive(&sm.kfull[s], lane);
-      if (lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
-      if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
-      // 32-token blocks: a piece per unit, whose slots 0..31 are its tokens
-      const bool small = a.bshift == 5;
+          for (int k = 0; k < 4; k++) x[k] = lds128(c + key * 128 + ch16 * 16 + 2048 * k);
+#pragma unroll
+          for (int k = 0; k < 4; k++) put16(f, x[k], to + k_to + 8192 * p + 2048 * k);
+        } else {
 #pragma unroll 1
-      for (int p = 0; p < (small ? 4 : 2); p++) {
-        if (!piece_full()) return;
-        const uint32_t c = c_s + at * kTreePiece;
-        const bool int4 = fmt >> (small ? p : 2 * p) & 1;
-        const TreeCodec f(int4);
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int ch = v_ch + 64 * i, chunk = v_pos ^ (ch >> (int4 ? 2 : 1) & 3);  // slots 16 chunk ..
-          const uint32_t from = c + (int4 ? ch * 32 + v_pos * 8 : ch * 64 + v_pos * 16);
-          const int to = small ? 4 * (p & 1) + 2 * chunk : 2 * chunk;
-          if (!small || chunk < 2)
-            sixteen(f, int4, from, vst + (small ? p >> 1 : p) * kTreeSlab + ch * 128 + ((to ^ (ch & 7)) << 4));
+          for (int i = 0; i < 4; i++) {
+            const bool int4 = fmt >> (2 * p + i / 2) & 1;
+            const int k = key + 16 * (i & 1);
+            put16(TreeCodec(int4), get16(int4, c + 4096 * (i / 2) + (int4 ? k * 64 + ch16 * 8 : k * 128 + ch16 * 16)),
+                  to + k_to + 8192 * p + 2048 * i);
+          }
         }
         piece_done();
       }
-      warp_arrive(&sm.vfull[s], lane);
+    } else {
+      if ((fmt & 15) == 0 && !small) {
+        const TreeCodec f(false);
+        const uint32_t v_to = v_ch * 128 + (((2 * (v_pos ^ (v_ch >> 1 & 3))) ^ (v_ch & 7)) << 4);
+#pragma unroll 1
+        for (int p = 0; p < 2; p++) {
+          if (!piece_full()) return;
+          const uint32_t c = c_s + at * kPiece;
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; k++) x[k] = lds128(c + tid * 16 + 2048 * k);
+#pragma unroll
+          for (int k = 0; k < 4; k++) put16(f, x[k], to + v_to + p * kTreeSlab + 4096 * k);
+          piece_done();
+        }
+      } else {
+        // 64-slot tiles of a pair of units, or (32-token blocks) of one, whose
+        // slots 0..31 are its tokens
+#pragma unroll 1
+        for (int p = 0; p < (small ? 4 : 2); p++) {
+          if (!piece_full()) return;
+          const uint32_t c = c_s + at * kPiece;
+          const bool int4 = fmt >> (small ? p : 2 * p) & 1;
+          const TreeCodec f(int4);
+#pragma unroll 1
+          for (int k = 0; k < 4; k++) {
+            const int ch = v_ch + 32 * k, chunk = v_pos ^ (ch >> (int4 ? 2 : 1) & 3);  // slots 16 chunk ..
+            const int c8 = small ? 4 * (p & 1) + 2 * chunk : 2 * chunk;
+            if (!small || chunk < 2)
+              put16(f, get16(int4, c + (int4 ? ch * 32 + v_pos * 8 : ch * 64 + v_pos * 16)),
+                    to + (small ? p >> 1 : p) * kTreeSlab + ch * 128 + ((c8 ^ (ch & 7)) << 4));
+          }
+          piece_done();
+        }
+      }
     }
-    if ((kF16 || !cold) && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+    warp_arrive(&full[s], lane);
+    // the record is ready for the softmax: with V's part of a tail tile
+    if (kV == !cold && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
   }
 }
 
@@ -445,92 +478,96 @@ __device__ __forceinline__ void bulk_to(uint32_t dst, const void *src, uint32_t 
       : "memory");
 }
 
-// One thread brings the bytes of the cold tiles: per tile K of units 0, 1 and 2,
-// 3 (4096 bytes apart), then their V tiles (32-token blocks: one per unit); FP16
-// rows 16 at a time.
+// One thread brings the bytes of the cold tiles: per tile K of two units (4096
+// bytes apart) and of the other two to one ring, their V tiles (32-token blocks:
+// one per unit) to the other; FP16 rows 16 at a time to one ring.  It alone
+// waits here, so its waits need no vote.
 template <int MT, bool kF16>
 __device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t c_s, int n) {
-  constexpr int kPieces = TreeSmem<MT>::kPieces;
-  const int lane = threadIdx.x & 31;
+  constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2;
   const uint64_t policy = l2_policy_evict_first();
   const bool small = a.bshift == 5;
-  int at = 0, sent = 0;
-  uint32_t turn = 0;
+  int at[2] = {0, 0}, sent[2] = {0, 0};  // by ring
+  uint32_t turn[2] = {0, 0};
+  auto room = [&](int ring) { return tree_wait_one(sm, &sm.cempty[ring * kRing + at[ring]], turn[ring] ^ 1, a); };
+  auto next = [&](int ring) {
+    sent[ring]++;
+    if (++at[ring] == kRing) {
+      at[ring] = 0;
+      turn[ring] ^= 1;
+    }
+  };
   bool ok = true;
   for (int j = 0; j < n && ok; j++) {
     if (j % kTreeBatch == 0) {
       const int batch = j / kTreeBatch;
-      if (!tree_wait(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
+      if (!tree_wait_one(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
     }
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
     if (!(r.flags & kTileCold)) continue;
-    const int pieces = kF16 ? 8 : small ? 6 : 4;
     const uint32_t fmt = r.fmt;
+    if constexpr (kF16) {
 #pragma unroll 1
-    for (int p = 0; p < pieces; p++) {
-      ok = tree_wait(sm, &sm.cempty[at], turn ^ 1, a);
-      if (!ok) break;
-      // the piece: up to two parts {source, bytes, place}
-      const uint8_t *src[2] = {nullptr, nullptr};
-      uint32_t bytes[2] = {0, 0};
-      if (kF16) {
-        if (r.at[p >> 1]) {
-          src[0] = r.at[p >> 1] + (p & 1) * kTreePiece;
-          bytes[0] = kTreePiece;
-        }
-      } else if (p < 2) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int u = 2 * p + i;
-          if (r.at[u]) {
-            bytes[i] = fmt >> u & 1 ? 2048 : 4096;
-            src[i] = r.at[u] + (fmt >> (4 + u) & 1 ? bytes[i] : 0);
-          }
-        }
-      } else {
-        const int u = small ? p - 2 : 2 * (p - 2);
-        if (r.at[u]) {
-          src[0] = r.at[u] + kTileBytes;
-          bytes[0] = fmt >> u & 1 ? kTileBytes / 2 : kTileBytes;
-        }
+      for (int p = 0; p < 8 && ok; p++) {
+        ok = room(0);
+        if (!ok) break;
+        const uint8_t *src = r.at[p >> 1];
+        uint64_t *bar = &sm.cfull[at[0]];
+        mbar_arrive_expect_tx(bar, src ? kPiece : 0);
+        if (src) bulk_to(c_s + at[0] * kPiece, src + (p & 1) * kPiece, kPiece, bar, policy);
+        next(0);
       }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.cfull[at], bytes[0] + bytes[1]);
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-          if (bytes[i]) bulk_to(c_s + at * kTreePiece + 4096 * i, src[i], bytes[i], &sm.cfull[at], policy);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < 4 && ok; u += 2) {
+        ok = room(0);
+        if (!ok) break;
+        const uint8_t *p0 = r.at[u], *p1 = r.at[u + 1];
+        const uint32_t n0 = !p0 ? 0 : fmt >> u & 1 ? 2048 : 4096, n1 = !p1 ? 0 : fmt >> (u + 1) & 1 ? 2048 : 4096;
+        uint64_t *bar = &sm.cfull[at[0]];
+        const uint32_t to = c_s + at[0] * kPiece;
+        mbar_arrive_expect_tx(bar, n0 + n1);
+        if (p0 == p1 && n0 == 4096) {  // the two halves of an INT8 tile are one run
+          bulk_to(to, p0, kPiece, bar, policy);
+        } else {
+          if (n0) bulk_to(to, p0 + (fmt >> (4 + u) & 1 ? n0 : 0), n0, bar, policy);
+          if (n1) bulk_to(to + 4096, p1 + (fmt >> (5 + u) & 1 ? n1 : 0), n1, bar, policy);
+        }
+        next(0);
       }
-      __syncwarp();
-      sent++;
-      if (++at == kPieces) {
-        at = 0;
-        turn ^= 1;
+#pragma unroll 1
+      for (int t = 0; t < (small ? 4 : 2) && ok; t++) {
+        ok = room(1);
+        if (!ok) break;
+        const int u = small ? t : 2 * t;
+        const uint8_t *src = r.at[u];
+        const uint32_t bytes = !src ? 0 : fmt >> u & 1 ? kTileBytes / 2 : kTileBytes;
+        uint64_t *bar = &sm.cfull[kRing + at[1]];
+        mbar_arrive_expect_tx(bar, bytes);
+        if (src) bulk_to(c_s + (kRing + at[1]) * kPiece, src + kTileBytes, bytes, bar, policy);
+        next(1);
       }
     }
   }
   // the copies in flight land before the CTA ends, also when nobody takes them
-  for (int i = 0; i < kPieces && i < sent; i++) {
-    if (--at < 0) {
-      at = kPieces - 1;
-      turn ^= 1;
+#pragma unroll
+  for (int ring = 0; ring < (kF16 ? 1 : 2); ring++) {
+    for (int i = 0; i < kRing && i < sent[ring]; i++) {
+      if (--at[ring] < 0) {
+        at[ring] = kRing - 1;
+        turn[ring] ^= 1;
+      }
+      mbar_wait_bounded(&sm.cfull[ring * kRing + at[ring]], turn[ring], kDefaultWaitCycles);
     }
-    mbar_wait_bounded(&sm.cfull[at], turn, kDefaultWaitCycles);
   }
 }
 
 // ---- the scout ----
 
-// [p, p + bytes) on its way into L2; 16-byte aligned.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-// The query rows of a unit into its Q operand(s), one arrival per lane when they
-// are there (rows beyond the tree keep what they were: nobody reads their
-// results).
+// The query rows of a unit on their way into its Q operand(s) (rows beyond the
+// tree keep what they were: nobody reads their results).
 template <int MT>
-__device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg, int rows, uint32_t st, uint64_t *bar,
-                                        int lane) {
+__device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg, int rows, uint32_t st, int lane) {
   const int G = a.group, n = min(128 * MT, rows - mg * 128 * MT), c = lane & 15;
   const __half *q = a.q + (static_cast<size_t>(b) * a.max_tree * a.hq + hk * G) * kDim + 8 * c;
   const uint32_t slab = MT == 1 ? a.q_rows * 128 : kTreeSlab, to = st + (c >> 3) * slab;
@@ -542,7 +579,6 @@ __device__ __forceinline__ void fetch_q(const TreeArgs &a, int b, int hk, int mg
                  "l"(q + (static_cast<size_t>(t) * a.hq + row - t * G) * kDim)
                  : "memory");
   }
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Lane 4 k + c looks up unit c of tile k of a batch.
@@ -591,20 +627,11 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
         const size_t i = static_cast<size_t>(phys) * a.hkv + hk;
         if (kF16) {
           at = a.cold + ((i << a.bshift) + slot) * kHotTokenBytes;
-          prefetch_l2(at, 32 * kHotTokenBytes);
         } else {
           at = a.cold + ((i << a.lsub) + (slot >> 6)) * kTilePairBytes;
           sc = __ldg(reinterpret_cast<const float2 *>(a.scales) + i);
           if (a.quant_bits == 4 || (a.n_int4 != nullptr && block < a.n_int4[b])) fmt |= 1;
           if (slot & 32) fmt |= 16;
-          if (!(slot & 32)) {  // the unit with the first slots brings the tile pair
-            if (fmt & 1) {
-              prefetch_l2(at, kTileBytes / 2);
-              prefetch_l2(at + kTileBytes, kTileBytes / 2);
-            } else {
-              prefetch_l2(at, kTilePairBytes);
-            }
-          }
         }
       }
     }
@@ -665,13 +692,15 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
         if (!tree_wait(sm, &sm.qempty[i][st], ((q_count >> (8 * at) & 1) ^ 1), a)) return;
         q_use &= ~(1u << at);
       }
+      fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * 256 * a.q_rows, lane);
       for (int st = 0; st < 2; st++)
         if (MT == 2 || fleft > 0 || (fj & 1) == st) {
           const int at = 2 * i + st;
           q_use |= 1u << at;
           q_count = (q_count & ~(255u << (8 * at))) | (((q_count >> (8 * at)) + 1) & 255u) << (8 * at);
+          // one arrival per lane when its rows are there
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sm.qfull[i][st])) : "memory");
         }
-      fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * 256 * a.q_rows, &sm.qfull[i], lane);
     }
     pos += kTreeBatch;
   }
@@ -686,7 +715,8 @@ __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, ui
                                          uint32_t tmem, int n, int i) {
   constexpr uint32_t idesc = tc_idesc_f16(128);
   const uint32_t t_s = tmem + 128 * i, t_p = t_s + 64, t_o = tmem + 256 + 128 * i;
-  int used = 0, begun = 0;  // tiles and segments of the stream
+  int used = 0, begun = 0;    // tiles and segments of the stream
+  uint32_t q_used = 0;        // bit b: segments of the stream in Q buffer b, modulo 2
   for (int j = MT == 1 ? i : 0; j < n; j += MT == 1 ? 2 : 1, used++) {
     const int s = j & (kTreeStages - 1);
     const uint32_t ph = (j / kTreeStages) & 1;
@@ -697,7 +727,10 @@ __device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, ui
     const int qb = a.q_bufs == 2 ? seg & 1 : 0;  // the segment's Q buffer
     const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
     const bool last = MT == 1 ? r.left < 2 : flags & kTileLast;
-    if (first && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return;
+    if (first) {
+      if (!tree_wait(sm, &sm.qfull[qb][i], q_used >> qb & 1, a)) return;
+      q_used ^= 1u << qb;
+    }
     fence_proxy_async_smem();
     tc_fence_after();
     {
@@ -788,7 +821,7 @@ __device__ __forceinline__ uint32_t tree_nodes(const TreeRec &r, int c, int k, u
   uint32_t own = 0, bad = 0;
   if (k >= 0) own = k < 64 ? static_cast<uint32_t>(nodes >> k) : 0u;
   else if (k > -32) own = static_cast<uint32_t>(nodes << -k);
-  bad = (r.bad[2 * c] | r.bad[2 * c + 1]) & own;
+  bad = (r.bad[0][c] | r.bad[1][c] | r.bad[2][c] | r.bad[3][c]) & own;
   if (bad) odd |= k >= 0 ? static_cast<uint64_t>(bad) << k : static_cast<uint64_t>(bad) >> -k;
   return own;
 }
@@ -1044,11 +1077,14 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
 template <int MT, bool kF16>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using Shape = TreeShape<MT>;
-  extern __shared__ uint8_t raw[];
-  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  const uint32_t base = smem_addr(raw);
+  if (base & 1023) {  // (the operands' swizzle is one of addresses)
+    set_status(a.status, HYB_STATUS_TIMEOUT);
+    return;
+  }
   const uint32_t q_s = base, k_s = q_s + Shape::kQBytes, v_s = k_s + kTreeStages * kTreeOperand, c_s = base + Shape::kTiles;
-  TreeSmem<MT> &sm = *reinterpret_cast<TreeSmem<MT> *>(raw + (base - smem_addr(raw)) + Shape::kTiles +
-                                                       TreeSmem<MT>::kPieces * kTreePiece);
+  TreeSmem<MT> &sm = *reinterpret_cast<TreeSmem<MT> *>(raw + Shape::kTiles + TreeSmem<MT>::kPieces * kPiece);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end
   constexpr int kMmaWarp = kTreeSoft + kTreeProd, kScoutWarp = kMmaWarp + kTreeMma;
@@ -1074,8 +1110,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     a.shared_units[blockIdx.x] = make_int4(0, 0, 0, 0);
     sm.abort = 0;
     for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.kfull[i], kTreeProd);
-      mbar_init(&sm.vfull[i], kTreeProd);
+      mbar_init(&sm.kfull[i], kTreeProd / 2);
+      mbar_init(&sm.vfull[i], kTreeProd / 2);
       mbar_init(&sm.kempty[i], MT);
       mbar_init(&sm.vempty[i], MT);
       mbar_init(&sm.rfull[i], 1);
@@ -1086,15 +1122,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       mbar_init(&sm.ofree[i], 8);
       mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd);
+    for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd / 2);
     for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.qfull[i], 32);
+      mbar_init(&sm.qfull[i][0], 32);
+      mbar_init(&sm.qfull[i][1], 32);
       mbar_init(&sm.qempty[i][0], 1);
       mbar_init(&sm.qempty[i][1], 1);
     }
     for (int i = 0; i < TreeSmem<MT>::kPieces; i++) {
       mbar_init(&sm.cfull[i], 1);
-      mbar_init(&sm.cempty[i], kTreeProd);
+      mbar_init(&sm.cempty[i], kF16 ? kTreeProd : kTreeProd / 2);
     }
     mbar_init(&sm.xfull, 8);
     mbar_fence_init();
@@ -1136,7 +1173,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     tree_softmax<MT>(a, sm, tmem, n_tiles);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeProdRegs));
-    tree_produce<MT, kF16>(a, sm, k_s, v_s, c_s, n_tiles);
+    if (warp < kTreeSoft + kTreeProd / 2) tree_produce<MT, kF16, false>(a, sm, k_s, c_s, n_tiles);
+    else tree_produce<MT, kF16, true>(a, sm, v_s, c_s, n_tiles);
   } else if (warp < kScoutWarp) {
     const int i = warp - kMmaWarp;
     tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
@@ -1147,7 +1185,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);
     __syncwarp();
   } else if (warp > kScoutWarp) {
-    tree_copy<MT, kF16>(a, sm, c_s, n_tiles);
+    if (lane == 0) tree_copy<MT, kF16>(a, sm, c_s, n_tiles);
+    __syncwarp();
   } else {
     tree_scout<MT, kF16>(a, sm, q_s, n_tiles);
     asm volatile("cp.async.wait_all;" ::: "memory");

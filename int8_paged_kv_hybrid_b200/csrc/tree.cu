@@ -27,14 +27,12 @@
 // L2 and fetches the query rows; a copy warp brings their bytes into a ring in
 // shared memory by bulk copies; four producer warps turn K, four V, from codes
 // or rows into FP16 in the 128-byte swizzled layout of the MMA's shared
-// operands; two groups
-// of four softmax warps (one query row per thread) keep two softmax streams and
-// write the weights over the logits in TMEM, where the second product reads
-// them as its A operand; a warp for each stream issues its MMAs.  The streams
-// are the two row tiles (MT 2), or the even and the odd tiles of the run (MT
-// 1), merged at a unit's end.  (Codes fetched by the producers' own loads, into
-// registers, made every other warp wait behind them in the load unit: 360 us
-// where this takes a fraction of it.)
+// operands; two groups of four softmax warps (one query row per thread) keep two
+// softmax streams and write the weights over the logits in TMEM, where the
+// second product reads them as its A operand.  The streams are the two row
+// tiles (MT 2, with an MMA warp each), or the two halves of every tile's keys
+// (MT 1), merged at a unit's end: then a tile's softmax is 64 keys per thread,
+// and S has two buffers, so that Q K^T of the next tile runs behind it.
 #include "kernels.cuh"
 #include "spec.cuh"
 #include "tc05.cuh"
@@ -57,11 +55,11 @@ constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeMma = 2;
 constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + kTreeMma + 2);
 constexpr int kTreeSoftRegs = 112, kTreeProdRegs = 80;
 
-// TreeRec::flags: the first, the second and the last tile of its segment (the
-// part of a unit that this CTA has); every key attended by every row and no
+// TreeRec::flags: the first and the last tile of its segment (the part of a unit
+// that this CTA has); every key attended by every row and no
 // negative scale; cold (not ring and nodes); the segment has the unit's first,
 // its last tile; the segment's number modulo 4
-constexpr uint32_t kTileFirst = 1, kTileSecond = 2, kTileLast = 4, kTilePlain = 8, kTileCold = 16, kUnitStart = 32,
+constexpr uint32_t kTileFirst = 1, kTileLast = 4, kTilePlain = 8, kTileCold = 16, kUnitStart = 32,
                    kUnitEnd = 64;
 constexpr int kTileSegShift = 7;
 
@@ -75,8 +73,7 @@ struct TreeRec {
   uint32_t fmt;          // bit c: unit c is INT4; bit 4 + c: it is the second half of its slots
   uint32_t flags;
   float v_max;           // largest |v_scale|
-  int left;              // tiles of the segment after this one
-  int rest;              // tiles of the unit after this one
+  int rest;              // tiles of the unit after the segment
   int b, hk, mg;         // the unit's sequence, kv head and row group
   int rows;              // query rows of the sequence and kv head
   // tail: its first row (ring rows in the order of their positions, then
@@ -95,15 +92,15 @@ template <int MT>
 struct TreeSmem {
   // pieces of 8192 bytes: a ring of codes of K and one of V, or one of FP16 rows
   static constexpr int kPieces = MT == 1 ? 6 : 4;
-  // MMA operands: MT 1 stage and stream are one; MT 2 both streams free a stage
+  // MMA operands (MT 2: both MMA warps free a stage)
   uint64_t kfull[kTreeStages], kempty[kTreeStages], vfull[kTreeStages], vempty[kTreeStages];
   uint64_t cfull[kPieces], cempty[kPieces];
   uint64_t rfull[2], rfree[2];     // records, by batch parity
   uint64_t mfull[kTreeRecs];       // a record's tile is in shared memory
-  // Q by buffer and stream: a stream sits out segments of one tile, and must
-  // not miss a phase of its barriers
-  uint64_t qfull[2][2], qempty[2][2];
-  uint64_t sfull[2], pfull[2], odone[2], ofree[2];  // by stream
+  uint64_t qfull[2], qempty[2];
+  uint64_t sfull[2];               // MT 1: by S buffer; MT 2: by stream
+  uint64_t pfull[2][2];            // by stream and (MT 1) S buffer
+  uint64_t odone[2], ofree[2];     // by stream
   uint64_t xfull;                  // MT 1: both streams' rows are in `stat`
   uint64_t drain[2];
   TreeRec rec[kTreeRecs];
@@ -589,7 +586,6 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
   int b = sm.start_b, segs = 0;     // segments begun before the batch
   TreeSeq q = tree_seq<MT>(a, b);
   long long pos = sm.start_pos + k; // the lane's tile within sequence b
-  uint32_t q_use = 0, q_count = 0;  // Q buffer i, stream s: bit 2 i + s in use; byte 2 i + s: its phases so far
 
   for (int j0 = 0, batch = 0; j0 < n; j0 += kTreeBatch, batch++) {
     const int j = j0 + k;
@@ -659,11 +655,10 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       if (c == 0) {
         r.fmt = fmt;
         r.v_max = v_max;
-        r.flags = (in == 0 ? kTileFirst : in == 1 ? kTileSecond : 0) | (left == 0 ? kTileLast : 0) |
+        r.flags = (in == 0 ? kTileFirst : 0) | (left == 0 ? kTileLast : 0) |
                   (plain ? kTilePlain : 0) | (cold ? kTileCold : 0) | (t <= j ? kUnitStart : 0) |
                   (left == q.tiles - 1 - t ? kUnitEnd : 0) | static_cast<uint32_t>(seg & 3) << kTileSegShift;
-        r.left = left;
-        r.rest = q.tiles - 1 - t;
+        r.rest = q.tiles - 1 - t - left;
         r.b = b;
         r.hk = hk;
         r.mg = mg;
@@ -685,90 +680,127 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       const int from = __ffs(f) - 1, i = a.q_bufs == 2 ? s & 1 : 0;
       const int fb = __shfl_sync(0xffffffffu, b, from), fhk = __shfl_sync(0xffffffffu, hk, from);
       const int fmg = __shfl_sync(0xffffffffu, mg, from), frows = __shfl_sync(0xffffffffu, rows, from);
-      const int fleft = __shfl_sync(0xffffffffu, left, from), fj = __shfl_sync(0xffffffffu, j, from);
-      for (int st = 0; st < 2; st++) {  // the streams that read the buffer last
-        const int at = 2 * i + st;
-        if (!(q_use >> at & 1)) continue;
-        if (!tree_wait(sm, &sm.qempty[i][st], ((q_count >> (8 * at) & 1) ^ 1), a)) return;
-        q_use &= ~(1u << at);
-      }
+      // (the buffer's last segment: a.q_bufs ago)
+      const uint32_t turn = a.q_bufs == 2 ? s >> 1 : s;
+      if (!tree_wait(sm, &sm.qempty[i], (turn & 1) ^ 1, a)) return;
       fetch_q<MT>(a, fb, fhk, fmg, frows, q_s + i * 256 * a.q_rows, lane);
-      for (int st = 0; st < 2; st++)
-        if (MT == 2 || fleft > 0 || (fj & 1) == st) {
-          const int at = 2 * i + st;
-          q_use |= 1u << at;
-          q_count = (q_count & ~(255u << (8 * at))) | (((q_count >> (8 * at)) + 1) & 255u) << (8 * at);
-          // one arrival per lane when its rows are there
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sm.qfull[i][st])) : "memory");
-        }
+      // one arrival per lane when its rows are there
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sm.qfull[i])) : "memory");
     }
     pos += kTreeBatch;
   }
 }
 
 // ---- the MMA warps (one elected thread issues) ----
-// TMEM columns: S of stream i at 128 i, its O at 256 + 128 i.  The weights of a
-// tile replace the upper half of its S (FP16, 64 columns).
+// TMEM columns: O of stream i at 256 + 128 i.  MT 1: S of tile j at 128 (j % 2),
+// its halves of 64 keys the streams'.  MT 2: S of stream i at 128 i.  The weights
+// (FP16, half the columns) replace S: MT 1 the first half of the stream's 64
+// columns, MT 2 the second half of the 128.
 
-template <int MT>
-__device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
-                                         uint32_t tmem, int n, int i) {
-  constexpr uint32_t idesc = tc_idesc_f16(128);
-  const uint32_t t_s = tmem + 128 * i, t_p = t_s + 64, t_o = tmem + 256 + 128 * i;
-  int used = 0, begun = 0;    // tiles and segments of the stream
-  uint32_t q_used = 0;        // bit b: segments of the stream in Q buffer b, modulo 2
-  for (int j = MT == 1 ? i : 0; j < n; j += MT == 1 ? 2 : 1, used++) {
-    const int s = j & (kTreeStages - 1);
-    const uint32_t ph = (j / kTreeStages) & 1;
-    // S = Q K^T (it replaces the weights of the stream's last P V)
-    if (!tree_wait(sm, &sm.kfull[s], ph, a)) return;
-    const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-    const uint32_t flags = r.flags, seg = flags >> kTileSegShift & 3;
-    const int qb = a.q_bufs == 2 ? seg & 1 : 0;  // the segment's Q buffer
-    const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
-    const bool last = MT == 1 ? r.left < 2 : flags & kTileLast;
-    if (first) {
-      if (!tree_wait(sm, &sm.qfull[qb][i], q_used >> qb & 1, a)) return;
-      q_used ^= 1u << qb;
-    }
+__device__ __forceinline__ void issue_qk(uint32_t t_s, uint32_t q, uint32_t q_slab, uint32_t k) {
+  const uint64_t dq = tc_desc_sw128(q), dk = tc_desc_sw128(k);
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    tc_mma_ss(t_s, dq + (i >> 2) * (q_slab >> 4) + 2 * (i & 3), dk + (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3),
+              tc_idesc_f16(128), i > 0);
+}
+
+// kSteps of 16 keys
+template <int kSteps>
+__device__ __forceinline__ void issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v, bool first) {
+  const uint64_t dv = tc_desc_sw128(v);
+#pragma unroll
+  for (int i = 0; i < kSteps; i++)
+    tc_mma_ts(t_o, t_p + 8 * i, dv + (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3), tc_idesc_f16(128), !first || i > 0);
+}
+
+// MT 1: one warp, Q K^T of the next tile before P V of this one.
+__device__ __forceinline__ void tree_mma1(const TreeArgs &a, TreeSmem<1> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
+                                          uint32_t tmem, int n) {
+  uint32_t flags = 0, next = 0;
+  auto qk = [&](int j) -> bool {
+    const int s = j & 1;
+    if (!tree_wait(sm, &sm.kfull[s], (j >> 1) & 1, a)) return false;
+    next = sm.rec[j & (kTreeRecs - 1)].flags;
+    const uint32_t seg = next >> kTileSegShift & 3;
+    const int qb = a.q_bufs == 2 ? seg & 1 : 0;
+    if ((next & kTileFirst) && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return false;
     fence_proxy_async_smem();
     tc_fence_after();
-    {
-      const uint64_t dq = tc_desc_sw128(q_s + (MT == 2 ? i * kTreeOperand : qb * 256 * a.q_rows));
-      const uint32_t q_slab = MT == 1 ? a.q_rows * 8 : kTreeSlab >> 4;
-      const uint64_t dk = tc_desc_sw128(k_s + s * kTreeOperand);
-      if (tc_elect()) {
+    if (tc_elect()) {
+      issue_qk(tmem + 128 * s, q_s + qb * 256 * a.q_rows, a.q_rows * 128, k_s + s * kTreeOperand);
+      tc_commit(&sm.sfull[s]);
+      tc_commit(&sm.kempty[s]);
+      if (next & kTileLast) tc_commit(&sm.qempty[qb]);
+    }
+    __syncwarp();
+    return true;
+  };
+  if (!qk(0)) return;
+  int begun = 0;  // segments
+  for (int j = 0; j < n; j++) {
+    const int s = j & 1;
+    const uint32_t ph = (j >> 1) & 1;
+    flags = next;
+    // (S of tile j + 1 replaces the weights of tile j - 1, whose P V is issued)
+    if (j + 1 < n && !qk(j + 1)) return;
+    const bool first = flags & kTileFirst;
+    if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const uint32_t o = 2 * (k & 3);
-          tc_mma_ss(t_s, dq + (k >> 2) * q_slab + o, dk + (k >> 2) * (kTreeSlab >> 4) + o, idesc, k > 0);
+    for (int i = 0; i < 2; i++) {
+      if (first && !tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
+      if (!tree_wait(sm, &sm.pfull[i][s], ph, a)) return;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      if (tc_elect()) {
+        issue_pv<4>(tmem + 256 + 128 * i, tmem + 128 * s + 64 * i, v_s + s * kTreeOperand + i * kTreeSlab, first);
+        if (flags & kTileLast) tc_commit(&sm.odone[i]);
+        if (i == 1) {
+          tc_commit(&sm.vempty[s]);
+          if ((j + 1) % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
         }
-        tc_commit(&sm.sfull[i]);
-        tc_commit(&sm.kempty[s]);
-        if (last) tc_commit(&sm.qempty[qb][i]);
       }
       __syncwarp();
     }
-    // O += P V
+    if (first) begun++;
+  }
+}
+
+// MT 2: a warp for each row tile i; S of the next tile replaces the weights of
+// this one.
+__device__ __forceinline__ void tree_mma2(const TreeArgs &a, TreeSmem<2> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
+                                          uint32_t tmem, int n, int i) {
+  const uint32_t t_s = tmem + 128 * i, t_o = tmem + 256 + 128 * i;
+  int begun = 0;  // segments
+  for (int j = 0; j < n; j++) {
+    const int s = j & 1;
+    const uint32_t ph = (j >> 1) & 1;
+    if (!tree_wait(sm, &sm.kfull[s], ph, a)) return;
+    const uint32_t flags = sm.rec[j & (kTreeRecs - 1)].flags;
+    const bool first = flags & kTileFirst;
+    if (first && !tree_wait(sm, &sm.qfull[0], begun & 1, a)) return;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    if (tc_elect()) {
+      issue_qk(t_s, q_s + i * kTreeOperand, kTreeSlab, k_s + s * kTreeOperand);
+      tc_commit(&sm.sfull[i]);
+      tc_commit(&sm.kempty[s]);
+      if (flags & kTileLast) tc_commit(&sm.qempty[0]);
+    }
+    __syncwarp();
     if (first) {
       if (!tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
       begun++;
     }
     if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
-    if (!tree_wait(sm, &sm.pfull[i], used & 1, a)) return;
+    if (!tree_wait(sm, &sm.pfull[i][0], j & 1, a)) return;
     fence_proxy_async_smem();
     tc_fence_after();
-    const uint64_t dv = tc_desc_sw128(v_s + s * kTreeOperand);
-    const bool batch_end = MT == 1 ? (j + 2) / kTreeBatch != j / kTreeBatch : (j + 1) % kTreeBatch == 0;
     if (tc_elect()) {
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const uint64_t o = (k >> 2) * (kTreeSlab >> 4) + 2 * (k & 3);
-        tc_mma_ts(t_o, t_p + 8 * k, dv + o, idesc, !first || k > 0);
-      }
+      issue_pv<8>(t_o, t_s + 64, v_s + s * kTreeOperand, first);
       tc_commit(&sm.vempty[s]);
-      if (last) tc_commit(&sm.odone[i]);
-      if (batch_end) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
+      if (flags & kTileLast) tc_commit(&sm.odone[i]);
+      if ((j + 1) % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
     }
     __syncwarp();
   }
@@ -867,26 +899,67 @@ __device__ __forceinline__ void tree_store_odd(const TreeArgs &a, uint64_t odd, 
   }
 }
 
+// Half a tile of logits: where keys are masked (or a scale is negative) S in v
+// becomes the logits, -inf where masked, and the factors of S become 1.
+__device__ __forceinline__ void tree_mask(const TreeRec &r, int h, bool tail, uint64_t nodes, uint64_t &odd, float &s0,
+                                          float &s1, uint32_t (&v)[64]) {
+  uint32_t ok0 = r.ok[2 * h], ok1 = r.ok[2 * h + 1];
+  if (tail) {
+    const int k = r.row0 - r.hot + 64 * h;
+    ok0 |= tree_nodes(r, 2 * h, k, nodes, odd);
+    ok1 |= tree_nodes(r, 2 * h + 1, k + 32, nodes, odd);
+  }
+#pragma unroll
+  for (int k = 0; k < 32; k++) {
+    v[k] = ok0 >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * s0) : 0xff800000u;
+    v[k + 32] = ok1 >> k & 1 ? __float_as_uint(__uint_as_float(v[k + 32]) * s1) : 0xff800000u;
+  }
+  s0 = s1 = 1.f;
+}
+
+// Its weights: exp2(logit - m), summed, and times the V scale over the
+// reference in FP16 to TMEM at `at`.
+__device__ __forceinline__ void tree_weights(const uint32_t (&v)[64], float s0, float s1, float f0, float f1, float minus_m,
+                                             uint32_t at, uint64_t &sum0, uint64_t &sum1) {
+  const uint64_t b2 = pack2(minus_m, minus_m);
+#pragma unroll
+  for (int u = 0; u < 2; u++) {
+    const uint64_t s2 = u ? pack2(s1, s1) : pack2(s0, s0), f2 = u ? pack2(f1, f1) : pack2(f0, f0);
+    uint32_t p[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float x, y;
+      unpack2(fma2(pack2(__uint_as_float(v[32 * u + k]), __uint_as_float(v[32 * u + k + 1])), s2, b2), x, y);
+      const uint64_t e = pack2(ex2(x), ex2(y));
+      if (k & 2) sum1 = add2(sum1, e);
+      else sum0 = add2(sum0, e);
+      unpack2(mul2(e, f2), x, y);
+      p[k >> 1] = half2_bits(x, y);
+    }
+    tc_st16(at + 16 * u, p);
+  }
+}
+
 template <int MT>
 __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t tmem, int n) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stream = warp >> 2, row_in = threadIdx.x & 127;
   const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  const uint32_t t_s = lanes + 128 * stream, t_p = t_s + 64, t_o = lanes + 256 + 128 * stream;
+  const uint32_t t_o = lanes + 256 + 128 * stream;
   const int part_row = (MT == 2 ? stream * 128 : 0) + row_in;
   // the row's state in the segment
   uint64_t odd = 0;  // attended nodes whose V is not finite
   float m = -INFINITY, l = 0.f, ref = 1.f;
-  int ends = 0;      // segments of the stream, and of those the merged ones (upper half)
-  uint32_t used = 0; // tiles of the stream
+  int ends = 0;      // segments
 
-  for (int j = MT == 1 ? stream : 0; j < n; j += MT == 1 ? 2 : 1, used++) {
-    if (!tree_wait(sm, &sm.sfull[stream], used & 1, a)) return;
+  for (int j = 0; j < n; j++) {
+    const int buf = MT == 1 ? j & 1 : stream;
+    if (!tree_wait(sm, &sm.sfull[buf], (MT == 1 ? j >> 1 : j) & 1, a)) return;
     if (!tree_wait(sm, &sm.mfull[j & (kTreeRecs - 1)], (j / kTreeRecs) & 1, a)) return;
     tc_fence_after();
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-    const uint32_t flags = r.flags;
-    const bool first = MT == 1 ? flags & (kTileFirst | kTileSecond) : flags & kTileFirst;
+    const uint32_t flags = r.flags, t_s = lanes + 128 * buf;
+    const bool first = flags & kTileFirst;
     const int row = r.mg * 128 * MT + part_row;  // of the sequence and kv head
     const bool live = row < r.rows, warp_live = row - lane < r.rows;
     if (first) {
@@ -896,90 +969,80 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
     }
     if (warp_live) {
       const bool tail = !(flags & kTileCold), plain = flags & kTilePlain;
-      // the two halves of S; where keys are masked (or a scale is negative) S
-      // becomes the logits, -inf where masked
       uint64_t nodes = 0;  // nodes that the row attends
       if (tail && live && r.keys > 0) {
         const int t = row_node(a, row);
         nodes = a.mask ? a.mask[static_cast<size_t>(r.b) * a.max_tree + t] : (~0ull >> (63 - t));
         if (r.keys < 64) nodes &= (1ull << r.keys) - 1;
       }
-      float top = -INFINITY;
+      // m and r follow the maxima when they lag too far behind; O and l follow
+      // them
+      auto follow = [&](float top) -> bool {
+        const float v_max = r.v_max;
+        float ref_new = first ? 1.f : ref;
+        if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
+        const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
+        if (__any_sync(0xffffffffu, m_new != m || ref_new != ref)) {
+          if (!first) {
+            // (MT 2: the stream's last P V is done, as this tile's S came after it)
+            if (MT == 1 && !tree_wait(sm, &sm.vempty[(j - 1) & 1], ((j - 1) >> 1) & 1, a)) return false;
+            if (MT == 1) tc_fence_after();
+            const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
+            l *= f;
+            const float g = f * __fdividef(ref, ref_new);
 #pragma unroll 1
-      for (int h = 0; h < 2; h++) {
-        uint32_t v[64];
-        tc_ld64(t_s + 64 * h, v);
-        tc_wait_ld(v);
-        float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
-        if (!plain) {
-          uint32_t ok0 = r.ok[2 * h], ok1 = r.ok[2 * h + 1];
-          if (tail) {
-            const int k = r.row0 - r.hot + 64 * h;
-            ok0 |= tree_nodes(r, 2 * h, k, nodes, odd);
-            ok1 |= tree_nodes(r, 2 * h + 1, k + 32, nodes, odd);
-          }
+            for (int c = 0; c < 8; c++) {
+              uint32_t o[16];
+              tc_ld16(t_o + 16 * c, o);
+              tc_wait_ld(o);
 #pragma unroll
-          for (int k = 0; k < 32; k++) {
-            v[k] = ok0 >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * s0) : 0xff800000u;
-            v[k + 32] = ok1 >> k & 1 ? __float_as_uint(__uint_as_float(v[k + 32]) * s1) : 0xff800000u;
+              for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+              tc_st16(t_o + 16 * c, o);
+            }
           }
-          tc_st64(t_s + 64 * h, v);
-          s0 = s1 = 1.f;
+          m = m_new;
+          ref = ref_new;
         }
-        top = fmaxf(top, fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1));
-      }
-      if (!plain) tc_wait_st();
-      // m and r follow when they lag too far behind; O and l follow them (the
-      // stream's last P V is done: this tile's S came after it)
-      const float v_max = r.v_max;
-      float ref_new = first ? 1.f : ref;
-      if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
-      const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
-      if (__any_sync(0xffffffffu, m_new != m || ref_new != ref)) {
-        if (!first) {
-          const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
-          l *= f;
-          const float g = f * __fdividef(ref, ref_new);
-#pragma unroll 1
-          for (int c = 0; c < 8; c++) {
-            uint32_t o[16];
-            tc_ld16(t_o + 16 * c, o);
-            tc_wait_ld(o);
-#pragma unroll
-            for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
-            tc_st16(t_o + 16 * c, o);
-          }
-        }
-        m = m_new;
-        ref = ref_new;
-      }
-      const float inv = __fdividef(1.f, ref);
-      // the weights exp2(logit - m), summed, and times the V scale over the
-      // reference in FP16: they go over the second half of S
-      const float minus_m = m == -INFINITY ? 0.f : -m;
-      const uint64_t b2 = pack2(minus_m, minus_m);
+        return true;
+      };
       uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll 1
-      for (int h = 1; h >= 0; h--) {
+      if constexpr (MT == 1) {
+        const int h = stream;
         uint32_t v[64];
         tc_ld64(t_s + 64 * h, v);
+        float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
+        const float f0 = r.v_scale[2 * h], f1 = r.v_scale[2 * h + 1];
         tc_wait_ld(v);
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const float s = plain ? r.k_scale[2 * h + u] * a.qk_scale : 1.f, f = r.v_scale[2 * h + u] * inv;
-          const uint64_t s2 = pack2(s, s), f2 = pack2(f, f);
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(v[32 * u + k]), __uint_as_float(v[32 * u + k + 1])), s2, b2), x, y);
-            const uint64_t e = pack2(ex2(x), ex2(y));
-            if (k & 2) sum1 = add2(sum1, e);
-            else sum0 = add2(sum0, e);
-            unpack2(mul2(e, f2), x, y);
-            p[k >> 1] = half2_bits(x, y);
+        if (!plain) tree_mask(r, h, tail, nodes, odd, s0, s1, v);
+        if (!follow(fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1))) return;
+        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+        tree_weights(v, s0, s1, f0 * inv, f1 * inv, minus_m, t_s + 64 * h, sum0, sum1);
+      } else {
+        // S in two halves, twice: for the maximum and for the weights (which go
+        // over the second half)
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; h++) {
+          uint32_t v[64];
+          tc_ld64(t_s + 64 * h, v);
+          tc_wait_ld(v);
+          float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
+          if (!plain) {
+            tree_mask(r, h, tail, nodes, odd, s0, s1, v);
+            tc_st64(t_s + 64 * h, v);
           }
-          tc_st16(t_p + 32 * h + 16 * u, p);
+          top = fmaxf(top, fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1));
+        }
+        if (!plain) tc_wait_st();
+        if (!follow(top)) return;
+        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+        for (int h = 1; h >= 0; h--) {
+          uint32_t v[64];
+          tc_ld64(t_s + 64 * h, v);
+          tc_wait_ld(v);
+          const float s0 = plain ? r.k_scale[2 * h] * a.qk_scale : 1.f, s1 = plain ? r.k_scale[2 * h + 1] * a.qk_scale : 1.f;
+          tree_weights(v, s0, s1, r.v_scale[2 * h] * inv, r.v_scale[2 * h + 1] * inv, minus_m, t_s + 64 + 32 * h, sum0, sum1);
         }
       }
       float x, y;
@@ -988,31 +1051,27 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       tc_wait_st();
     }
     // what the segment's end needs of the record, which may be gone after pfull
-    const bool end = MT == 1 ? r.left < 2 : flags & kTileLast;
-    const bool merge = MT == 1 && (r.left > 0 || !(flags & kTileFirst));
-    const int b = r.b, hk = r.hk, mg = r.mg, rest = r.rest - r.left;
+    const int b = r.b, hk = r.hk, mg = r.mg, rest = r.rest;
     tc_fence_before();
-    warp_arrive(&sm.pfull[stream], lane);
-    if (!end) continue;
+    warp_arrive(&sm.pfull[stream][MT == 1 ? buf : 0], lane);
+    if (!(flags & kTileLast)) continue;
 
-    // O of the stream's last tile
+    // O of the segment's last tile
     const bool whole = (flags & kUnitStart) && (flags & kUnitEnd);
     const int t = row_node(a, row);
     const size_t out_row = (static_cast<size_t>(b) * a.max_tree + t) * a.hq + hk * a.group + row - t * a.group;
     const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (flags & kUnitStart ? 1 : 0);
     if (!tree_wait(sm, &sm.odone[stream], ends & 1, a)) return;
-    ends++;
     tc_fence_after();
     // both streams of a row meet: stream i takes channels 64 i.. of the two
     float g = ref, gx = 0.f;  // factors of this stream's O and of the other's
     int c0 = 0, c1 = kDim;
-    if (MT == 1 && merge) {
-      TreeStat *st = &sm.stat[ends >> 16 & 1][0][row_in];
+    if constexpr (MT == 1) {
+      TreeStat *st = &sm.stat[ends & 1][0][row_in];
       st[128 * stream] = TreeStat{m, l, ref, odd};
       tc_fence_before();
       warp_arrive(&sm.xfull, lane);
-      if (!tree_wait(sm, &sm.xfull, ends >> 16 & 1, a)) return;
-      ends += 1 << 16;
+      if (!tree_wait(sm, &sm.xfull, ends & 1, a)) return;
       tc_fence_after();
       const TreeStat x = st[128 * (stream ^ 1)];
       const float top = fmaxf(m, x.m);
@@ -1037,7 +1096,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         tc_wait_ld(o);
 #pragma unroll
         for (int k = 0; k < 16; k++) o[k] = g != 0.f ? __float_as_uint(__uint_as_float(o[k]) * g) : 0u;
-        if (MT == 1 && merge) {
+        if (MT == 1) {
           uint32_t w[16];
           tc_ld16(lanes + 256 + 128 * (stream ^ 1) + c, w);
           tc_wait_ld(w);
@@ -1049,13 +1108,13 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       }
       if (live && odd) tree_store_odd<MT>(a, odd, c0, c1, b, hk, whole, out_row, slot, part_row);
     }
-    // O is free: eight arrivals on its barrier, of both streams' warps or twice
-    // of this one's
+    // O is free (MT 1: both groups read both)
+    ends++;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&sm.ofree[stream]);
-      mbar_arrive(&sm.ofree[merge ? stream ^ 1 : stream]);
+      if (MT == 1) mbar_arrive(&sm.ofree[stream ^ 1]);
     }
     if (live && writer) {
       if (whole) {
@@ -1115,19 +1174,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       mbar_init(&sm.kempty[i], MT);
       mbar_init(&sm.vempty[i], MT);
       mbar_init(&sm.rfull[i], 1);
-      mbar_init(&sm.rfree[i], 2);
+      mbar_init(&sm.rfree[i], MT);
       mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.pfull[i], 4);
+      mbar_init(&sm.pfull[i][0], 4);
+      mbar_init(&sm.pfull[i][1], 4);
       mbar_init(&sm.odone[i], 1);
-      mbar_init(&sm.ofree[i], 8);
+      mbar_init(&sm.ofree[i], MT == 1 ? 8 : 4);
       mbar_init(&sm.drain[i], 1);
     }
     for (int i = 0; i < kTreeRecs; i++) mbar_init(&sm.mfull[i], kTreeProd / 2);
     for (int i = 0; i < 2; i++) {
-      mbar_init(&sm.qfull[i][0], 32);
-      mbar_init(&sm.qfull[i][1], 32);
-      mbar_init(&sm.qempty[i][0], 1);
-      mbar_init(&sm.qempty[i][1], 1);
+      mbar_init(&sm.qfull[i], 32);
+      mbar_init(&sm.qempty[i], MT);
     }
     for (int i = 0; i < TreeSmem<MT>::kPieces; i++) {
       mbar_init(&sm.cfull[i], 1);
@@ -1177,7 +1235,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     else tree_produce<MT, kF16, true>(a, sm, v_s, c_s, n_tiles);
   } else if (warp < kScoutWarp) {
     const int i = warp - kMmaWarp;
-    tree_mma<MT>(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
+    if constexpr (MT == 2) tree_mma2(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
+    else if (i == 0) tree_mma1(a, sm, q_s, k_s, v_s, tmem, n_tiles);
     __syncwarp();
     // no MMA is in flight when TMEM is given back
     if (tc_elect()) tc_commit(&sm.drain[i]);

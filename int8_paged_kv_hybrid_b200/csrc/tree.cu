@@ -151,35 +151,21 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   return s;
 }
 
-// Wait for phase `parity`; false when the wait or the kernel gave up.
-template <typename Sm>
-__device__ __forceinline__ bool tree_wait_slow(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  const bool quick = a.wait_cycles < kShortWaitCycles;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
-  while (!(quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
-    if (sm.abort) return false;
-    if (static_cast<uint32_t>(clock()) - t0 > a.wait_cycles) {
-      sm.abort = 1;
-      set_status(a.status, HYB_STATUS_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
-// ... by one thread,
-template <typename Sm>
-__device__ __forceinline__ bool tree_wait_one(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  return mbar_test_wait(bar, parity) || tree_wait_slow(sm, bar, parity, a);
-}
-
-// ... and by a whole warp, with one answer.
-template <typename Sm>
+// Wait for phase `parity`; false when the wait or the kernel gave up.  By a whole
+// warp, with one answer, or (kOne) by one thread.  Small, as it stands at many places.
+template <bool kOne = false, typename Sm>
 __device__ __forceinline__ bool tree_wait(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
-  bool ok = mbar_test_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  if (!ok) ok = tree_wait_slow(sm, bar, parity, a);
-  return __all_sync(0xffffffffu, ok);
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (;;) {
+    const bool ok = mbar_try_wait(bar, parity);
+    if (kOne ? ok : __all_sync(0xffffffffu, ok)) return true;
+    const uint32_t t = static_cast<uint32_t>(clock()) | 1;
+    if (t0 == 0) t0 = t;
+    if (kOne ? sm.abort || t - t0 > a.wait_cycles : __any_sync(0xffffffffu, sm.abort || t - t0 > a.wait_cycles)) break;
+  }
+  sm.abort = 1;
+  return false;
 }
 
 // The node of a query row: row / (Hq / Hkv), by a multiplication that is exact
@@ -307,28 +293,30 @@ __device__ __forceinline__ void tail_v(const TreeArgs &a, TreeRec &r, uint32_t v
 #pragma unroll 1
   for (int u = 0; u < 4; u++) {
     const uint64_t mine = reinterpret_cast<uint64_t>(tail_row(a, r, 32 * u + lane, 1));
-    uint32_t w[16];
-#pragma unroll
-    for (int k = 0; k < 16; k++) {
-      const uint64_t p = __shfl_sync(0xffffffffu, mine, k0 + k);
-      w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + 2 * pair)) : 0u;
-    }
-    // A node's V that is not finite must not meet the zero weight of a row that
-    // does not attend the node: it becomes 0 here and the record names the
-    // node; the rows that do attend it add it at the end
-    const int ring = r.hot - (r.row0 + 32 * u + k0);  // ring rows among the 16
     uint32_t bad = 0;
+#pragma unroll 1
+    for (int k8 = k0; k8 < k0 + 16; k8 += 8) {
+      uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-      uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
-      if (k < ring) nf = 0;
-      w[k] &= ~((nf >> 15) * 0xffffu);
-      bad |= nf ? 1u << k : 0u;
+      for (int k = 0; k < 8; k++) {
+        const uint64_t p = __shfl_sync(0xffffffffu, mine, k8 + k);
+        w[k] = p ? __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const __half *>(p) + 2 * pair)) : 0u;
+      }
+      // A node's V that is not finite must not meet the zero weight of a row that
+      // does not attend the node: it becomes 0 here and the record names the
+      // node; the rows that do attend it add it at the end
+      const int ring = r.hot - (r.row0 + 32 * u + k8);  // ring rows among the eight
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        uint32_t nf = ((w[k] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;  // bit 15 of a half: its exponent is all ones
+        if (k < ring) nf = 0;
+        w[k] &= ~((nf >> 15) * 0xffffu);
+        bad |= nf ? 1u << (k8 + k) : 0u;
+      }
+      put_v(vst, pair, 32 * u + k8, w);
     }
-    bad = __reduce_or_sync(0xffffffffu, bad << k0);
+    bad = __reduce_or_sync(0xffffffffu, bad);
     if (lane == 0) r.bad[tid >> 5][u] = bad;
-    put_v(vst, pair, 32 * u + k0, w);
-    put_v(vst, pair, 32 * u + k0 + 8, w + 8);
   }
 }
 
@@ -486,7 +474,7 @@ __device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, u
   const bool small = a.bshift == 5;
   int at[2] = {0, 0}, sent[2] = {0, 0};  // by ring
   uint32_t turn[2] = {0, 0};
-  auto room = [&](int ring) { return tree_wait_one(sm, &sm.cempty[ring * kRing + at[ring]], turn[ring] ^ 1, a); };
+  auto room = [&](int ring) { return tree_wait<true>(sm, &sm.cempty[ring * kRing + at[ring]], turn[ring] ^ 1, a); };
   auto next = [&](int ring) {
     sent[ring]++;
     if (++at[ring] == kRing) {
@@ -498,7 +486,7 @@ __device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, u
   for (int j = 0; j < n && ok; j++) {
     if (j % kTreeBatch == 0) {
       const int batch = j / kTreeBatch;
-      if (!tree_wait_one(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
+      if (!tree_wait<true>(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
     }
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
     if (!(r.flags & kTileCold)) continue;
@@ -585,27 +573,33 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
   const bool on = lane < 4 * kTreeBatch;
   int b = sm.start_b, segs = 0;     // segments begun before the batch
   TreeSeq q = tree_seq<MT>(a, b);
-  long long pos = sm.start_pos + k; // the lane's tile within sequence b
+  // the lane's tile: tile t of row group mg of kv head hk
+  int t = static_cast<int>(sm.start_pos % q.tiles), hk = static_cast<int>(sm.start_pos / q.tiles), mg = hk % q.groups;
+  hk /= q.groups;
+  t += k;
 
+#pragma unroll 1
   for (int j0 = 0, batch = 0; j0 < n; j0 += kTreeBatch, batch++) {
     const int j = j0 + k;
     const bool have = on && j < n;
-    int unit = 0, t = 0;
     if (have) {
-      for (;;) {
-        const long long span = static_cast<long long>(q.tiles) * q.groups * a.hkv;
-        if (pos < span) break;
-        pos -= span;
-        q = tree_seq<MT>(a, ++b);
+#pragma unroll 1
+      while (t >= q.tiles) {
+        t -= q.tiles;
+        if (++mg < q.groups) continue;
+        mg = 0;
+        if (++hk < a.hkv) continue;
+        hk = 0;
+#pragma unroll 1
+        do q = tree_seq<MT>(a, ++b);
+        while (q.groups == 0);
       }
-      unit = static_cast<int>(pos / q.tiles);
-      t = static_cast<int>(pos - static_cast<long long>(unit) * q.tiles);
     }
     const int in = min(t, j);                        // tiles of the segment before this one
     const int left = min(q.tiles - 1 - t, n - 1 - j);  // and after it
     const uint32_t firsts = __ballot_sync(0xffffffffu, have && in == 0 && c == 0);
     const int seg = segs + __popc(firsts & (0xffffffffu >> (31 - (4 * k)))) - 1;
-    const int hk = unit / q.groups, mg = unit - hk * q.groups, rows = q.nt * a.group;
+    const int rows = q.nt * a.group;
 
     const int p = t * kTK + 32 * c;  // the unit's first position
     const bool cold = t * kTK < q.cold;
@@ -687,82 +681,83 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
       // one arrival per lane when its rows are there
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sm.qfull[i])) : "memory");
     }
-    pos += kTreeBatch;
+    t += kTreeBatch;
   }
 }
 
 // ---- the MMA warps (one elected thread issues) ----
 // TMEM columns: O of stream i at 256 + 128 i.  MT 1: S of tile j at 128 (j % 2),
 // its halves of 64 keys the streams'.  MT 2: S of stream i at 128 i.  The weights
-// (FP16, half the columns) replace S: MT 1 the first half of the stream's 64
-// columns, MT 2 the second half of the 128.
+// (FP16) replace the first half of the stream's columns of S.
 
+// (Half of a product's steps unrolled: instructions that fit the caches near the
+// SM count for more than the loops' overhead.)
 __device__ __forceinline__ void issue_qk(uint32_t t_s, uint32_t q, uint32_t q_slab, uint32_t k) {
-  const uint64_t dq = tc_desc_sw128(q), dk = tc_desc_sw128(k);
+  uint64_t dq = tc_desc_sw128(q), dk = tc_desc_sw128(k);
+#pragma unroll 1
+  for (int h = 0; h < 2; h++, dq += q_slab >> 4, dk += kTreeSlab >> 4) {
 #pragma unroll
-  for (int i = 0; i < 8; i++)
-    tc_mma_ss(t_s, dq + (i >> 2) * (q_slab >> 4) + 2 * (i & 3), dk + (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3),
-              tc_idesc_f16(128), i > 0);
+    for (int i = 0; i < 4; i++) tc_mma_ss(t_s, dq + 2 * i, dk + 2 * i, tc_idesc_f16(128), h > 0 || i > 0);
+  }
 }
 
-// kSteps of 16 keys
-template <int kSteps>
+// 64 keys
 __device__ __forceinline__ void issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v, bool first) {
   const uint64_t dv = tc_desc_sw128(v);
 #pragma unroll
-  for (int i = 0; i < kSteps; i++)
-    tc_mma_ts(t_o, t_p + 8 * i, dv + (i >> 2) * (kTreeSlab >> 4) + 2 * (i & 3), tc_idesc_f16(128), !first || i > 0);
+  for (int i = 0; i < 4; i++) tc_mma_ts(t_o, t_p + 8 * i, dv + 2 * i, tc_idesc_f16(128), !first || i > 0);
 }
 
 // MT 1: one warp, Q K^T of the next tile before P V of this one.
 __device__ __forceinline__ void tree_mma1(const TreeArgs &a, TreeSmem<1> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
                                           uint32_t tmem, int n) {
-  uint32_t flags = 0, next = 0;
-  auto qk = [&](int j) -> bool {
-    const int s = j & 1;
-    if (!tree_wait(sm, &sm.kfull[s], (j >> 1) & 1, a)) return false;
-    next = sm.rec[j & (kTreeRecs - 1)].flags;
-    const uint32_t seg = next >> kTileSegShift & 3;
-    const int qb = a.q_bufs == 2 ? seg & 1 : 0;
-    if ((next & kTileFirst) && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return false;
-    fence_proxy_async_smem();
-    tc_fence_after();
-    if (tc_elect()) {
-      issue_qk(tmem + 128 * s, q_s + qb * 256 * a.q_rows, a.q_rows * 128, k_s + s * kTreeOperand);
-      tc_commit(&sm.sfull[s]);
-      tc_commit(&sm.kempty[s]);
-      if (next & kTileLast) tc_commit(&sm.qempty[qb]);
-    }
-    __syncwarp();
-    return true;
-  };
-  if (!qk(0)) return;
+  uint32_t flags = 0;
   int begun = 0;  // segments
-  for (int j = 0; j < n; j++) {
-    const int s = j & 1;
-    const uint32_t ph = (j >> 1) & 1;
-    flags = next;
-    // (S of tile j + 1 replaces the weights of tile j - 1, whose P V is issued)
-    if (j + 1 < n && !qk(j + 1)) return;
-    const bool first = flags & kTileFirst;
-    if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      if (first && !tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
-      if (!tree_wait(sm, &sm.pfull[i][s], ph, a)) return;
+#pragma unroll 1
+  for (int j = 0; j <= n; j++) {
+    uint32_t next = 0;
+    if (j < n) {
+      const int s = j & 1;
+      if (!tree_wait(sm, &sm.kfull[s], (j >> 1) & 1, a)) return;
+      next = sm.rec[j & (kTreeRecs - 1)].flags;
+      const uint32_t seg = next >> kTileSegShift & 3;
+      const int qb = a.q_bufs == 2 ? seg & 1 : 0;
+      if ((next & kTileFirst) && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return;
       fence_proxy_async_smem();
       tc_fence_after();
+      // (S replaces the weights of tile j - 2, whose P V is issued)
       if (tc_elect()) {
-        issue_pv<4>(tmem + 256 + 128 * i, tmem + 128 * s + 64 * i, v_s + s * kTreeOperand + i * kTreeSlab, first);
-        if (flags & kTileLast) tc_commit(&sm.odone[i]);
-        if (i == 1) {
-          tc_commit(&sm.vempty[s]);
-          if ((j + 1) % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
-        }
+        issue_qk(tmem + 128 * s, q_s + qb * 256 * a.q_rows, a.q_rows * 128, k_s + s * kTreeOperand);
+        tc_commit(&sm.sfull[s]);
+        tc_commit(&sm.kempty[s]);
+        if (next & kTileLast) tc_commit(&sm.qempty[qb]);
       }
       __syncwarp();
     }
-    if (first) begun++;
+    if (j > 0) {
+      const int s = (j - 1) & 1;
+      const uint32_t ph = ((j - 1) >> 1) & 1;
+      const bool first = flags & kTileFirst;
+      if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
+#pragma unroll 1
+      for (int i = 0; i < 2; i++) {
+        if (first && !tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
+        if (!tree_wait(sm, &sm.pfull[i][s], ph, a)) return;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (tc_elect()) {
+          issue_pv(tmem + 256 + 128 * i, tmem + 128 * s + 64 * i, v_s + s * kTreeOperand + i * kTreeSlab, first);
+          if (flags & kTileLast) tc_commit(&sm.odone[i]);
+          if (i == 1) {
+            tc_commit(&sm.vempty[s]);
+            if (j % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch - 1) & 1]);
+          }
+        }
+        __syncwarp();
+      }
+      if (first) begun++;
+    }
+    flags = next;
   }
 }
 
@@ -797,7 +792,8 @@ __device__ __forceinline__ void tree_mma2(const TreeArgs &a, TreeSmem<2> &sm, ui
     fence_proxy_async_smem();
     tc_fence_after();
     if (tc_elect()) {
-      issue_pv<8>(t_o, t_s + 64, v_s + s * kTreeOperand, first);
+#pragma unroll 1
+      for (int h = 0; h < 2; h++) issue_pv(t_o, t_s + 32 * h, v_s + s * kTreeOperand + h * kTreeSlab, first && h == 0);
       tc_commit(&sm.vempty[s]);
       if (flags & kTileLast) tc_commit(&sm.odone[i]);
       if ((j + 1) % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
@@ -899,45 +895,23 @@ __device__ __forceinline__ void tree_store_odd(const TreeArgs &a, uint64_t odd, 
   }
 }
 
-// Half a tile of logits: where keys are masked (or a scale is negative) S in v
-// becomes the logits, -inf where masked, and the factors of S become 1.
-__device__ __forceinline__ void tree_mask(const TreeRec &r, int h, bool tail, uint64_t nodes, uint64_t &odd, float &s0,
-                                          float &s1, uint32_t (&v)[64]) {
-  uint32_t ok0 = r.ok[2 * h], ok1 = r.ok[2 * h + 1];
-  if (tail) {
-    const int k = r.row0 - r.hot + 64 * h;
-    ok0 |= tree_nodes(r, 2 * h, k, nodes, odd);
-    ok1 |= tree_nodes(r, 2 * h + 1, k + 32, nodes, odd);
-  }
-#pragma unroll
-  for (int k = 0; k < 32; k++) {
-    v[k] = ok0 >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * s0) : 0xff800000u;
-    v[k + 32] = ok1 >> k & 1 ? __float_as_uint(__uint_as_float(v[k + 32]) * s1) : 0xff800000u;
-  }
-  s0 = s1 = 1.f;
-}
-
-// Its weights: exp2(logit - m), summed, and times the V scale over the
+// The weights of a unit: exp2(logit - m), summed, and times the V scale over the
 // reference in FP16 to TMEM at `at`.
-__device__ __forceinline__ void tree_weights(const uint32_t (&v)[64], float s0, float s1, float f0, float f1, float minus_m,
-                                             uint32_t at, uint64_t &sum0, uint64_t &sum1) {
-  const uint64_t b2 = pack2(minus_m, minus_m);
+__device__ __forceinline__ void tree_weights(const uint32_t (&v)[32], float scale, float factor, float minus_m, uint32_t at,
+                                             uint64_t &sum0, uint64_t &sum1) {
+  const uint64_t s2 = pack2(scale, scale), f2 = pack2(factor, factor), b2 = pack2(minus_m, minus_m);
+  uint32_t p[16];
 #pragma unroll
-  for (int u = 0; u < 2; u++) {
-    const uint64_t s2 = u ? pack2(s1, s1) : pack2(s0, s0), f2 = u ? pack2(f1, f1) : pack2(f0, f0);
-    uint32_t p[16];
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      float x, y;
-      unpack2(fma2(pack2(__uint_as_float(v[32 * u + k]), __uint_as_float(v[32 * u + k + 1])), s2, b2), x, y);
-      const uint64_t e = pack2(ex2(x), ex2(y));
-      if (k & 2) sum1 = add2(sum1, e);
-      else sum0 = add2(sum0, e);
-      unpack2(mul2(e, f2), x, y);
-      p[k >> 1] = half2_bits(x, y);
-    }
-    tc_st16(at + 16 * u, p);
+  for (int k = 0; k < 32; k += 2) {
+    float x, y;
+    unpack2(fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), s2, b2), x, y);
+    const uint64_t e = pack2(ex2(x), ex2(y));
+    if (k & 2) sum1 = add2(sum1, e);
+    else sum0 = add2(sum0, e);
+    unpack2(mul2(e, f2), x, y);
+    p[k >> 1] = half2_bits(x, y);
   }
+  tc_st16(at, p);
 }
 
 template <int MT>
@@ -1006,44 +980,39 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         return true;
       };
       uint64_t sum0 = 0, sum1 = 0;
-      if constexpr (MT == 1) {
-        const int h = stream;
-        uint32_t v[64];
-        tc_ld64(t_s + 64 * h, v);
-        float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
-        const float f0 = r.v_scale[2 * h], f1 = r.v_scale[2 * h + 1];
+      // S by units of 32 keys, twice: for the maximum and for the weights
+      constexpr int kUnits = MT == 1 ? 2 : 4;
+      const int u0 = MT == 1 ? 2 * stream : 0;
+      const uint32_t t_p = t_s + 32 * u0;
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int u = 0; u < kUnits; u++) {
+        uint32_t v[32];
+        tc_ld32(t_p + 32 * u, v);
+        float scale = r.k_scale[u0 + u] * a.qk_scale;
         tc_wait_ld(v);
-        if (!plain) tree_mask(r, h, tail, nodes, odd, s0, s1, v);
-        if (!follow(fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1))) return;
-        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
-        tree_weights(v, s0, s1, f0 * inv, f1 * inv, minus_m, t_s + 64 * h, sum0, sum1);
-      } else {
-        // S in two halves, twice: for the maximum and for the weights (which go
-        // over the second half)
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int h = 0; h < 2; h++) {
-          uint32_t v[64];
-          tc_ld64(t_s + 64 * h, v);
-          tc_wait_ld(v);
-          float s0 = r.k_scale[2 * h] * a.qk_scale, s1 = r.k_scale[2 * h + 1] * a.qk_scale;
-          if (!plain) {
-            tree_mask(r, h, tail, nodes, odd, s0, s1, v);
-            tc_st64(t_s + 64 * h, v);
-          }
-          top = fmaxf(top, fmaxf(max_of<32>(v) * s0, max_of<32>(v + 32) * s1));
+        if (!plain) {
+          // some keys are masked (or the scale is negative): the logits, -inf
+          // where masked, replace S
+          uint32_t ok = r.ok[u0 + u];
+          if (tail) ok |= tree_nodes(r, u0 + u, r.row0 - r.hot + 32 * (u0 + u), nodes, odd);
+#pragma unroll
+          for (int k = 0; k < 32; k++) v[k] = ok >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * scale) : 0xff800000u;
+          scale = 1.f;
+          tc_st32(t_p + 32 * u, v);
         }
-        if (!plain) tc_wait_st();
-        if (!follow(top)) return;
-        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+        top = fmaxf(top, max_of<32>(v) * scale);
+      }
+      if (!plain) tc_wait_st();
+      if (!follow(top)) return;
+      const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
 #pragma unroll 1
-        for (int h = 1; h >= 0; h--) {
-          uint32_t v[64];
-          tc_ld64(t_s + 64 * h, v);
-          tc_wait_ld(v);
-          const float s0 = plain ? r.k_scale[2 * h] * a.qk_scale : 1.f, s1 = plain ? r.k_scale[2 * h + 1] * a.qk_scale : 1.f;
-          tree_weights(v, s0, s1, r.v_scale[2 * h] * inv, r.v_scale[2 * h + 1] * inv, minus_m, t_s + 64 + 32 * h, sum0, sum1);
-        }
+      for (int u = 0; u < kUnits; u++) {
+        uint32_t v[32];
+        tc_ld32(t_p + 32 * u, v);
+        const float scale = plain ? r.k_scale[u0 + u] * a.qk_scale : 1.f, factor = r.v_scale[u0 + u] * inv;
+        tc_wait_ld(v);
+        tree_weights(v, scale, factor, minus_m, t_p + 16 * u, sum0, sum1);
       }
       float x, y;
       unpack2(add2(sum0, sum1), x, y);
@@ -1241,7 +1210,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     // no MMA is in flight when TMEM is given back
     if (tc_elect()) tc_commit(&sm.drain[i]);
     __syncwarp();
-    if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) set_status(a.status, HYB_STATUS_TIMEOUT);
+    if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) sm.abort = 1;
     __syncwarp();
   } else if (warp > kScoutWarp) {
     if (lane == 0) tree_copy<MT, kF16>(a, sm, c_s, n_tiles);
@@ -1254,6 +1223,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tc_dealloc(tmem, 512);
+  if (tid == 0 && sm.abort) set_status(a.status, HYB_STATUS_TIMEOUT);
 }
 
 // ---- the merge of units that several CTAs share ----

@@ -16,8 +16,10 @@ __host__ __device__ constexpr uint32_t tc_idesc_f16(int n) {
 // Shared-memory descriptor of a K-major operand in 128-byte swizzled rows
 // (64 FP16 values each; groups of eight rows are 1024 bytes apart), base
 // 1024-byte aligned.  A step of 16 values along K adds 32 bytes to the address.
-__device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t smem) {
-  return static_cast<uint64_t>((smem >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// (its low half; the high half is the same for all)
+__device__ __forceinline__ uint32_t tc_desc_low(uint32_t smem) { return ((smem >> 4) & 0x3fff) | (1u << 16); }
+__device__ __forceinline__ uint64_t tc_desc(uint32_t low) {
+  return static_cast<uint64_t>(64u | (1u << 14) | (2u << 29)) << 32 | low;
 }
 
 __device__ __forceinline__ void tc_alloc(uint32_t *slot, uint32_t cols) {  // one warp
@@ -46,20 +48,20 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, K = 16
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "l"(tc_desc(a)), "l"(tc_desc(b)), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, K = 16 (A: two FP16 values per column)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "r"(a), "l"(tc_desc(b)), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
 

@@ -263,12 +263,13 @@ __device__ __forceinline__ const __half *tail_row(const TreeArgs &a, const TreeR
 __device__ __forceinline__ void tail_k(const TreeArgs &a, const TreeRec &r, uint32_t kst, int tid) {
   const __half *p = tail_row(a, r, tid, 0);
 #pragma unroll 1
-  for (int half = 0; half < 2; half++) {
-    uint4 x[8];
+  for (int q = 0; q < 4; q++) {
+    uint4 x[4];
 #pragma unroll
-    for (int j = 0; j < 8; j++) x[j] = p ? ldg16(p + 64 * half + 8 * j) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 4; j++) x[j] = p ? ldg16(p + 32 * q + 8 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 8; j++) sts128(kst + half * kTreeSlab + tid * 128 + ((j ^ (tid & 7)) << 4), x[j]);
+    for (int j = 0; j < 4; j++)
+      sts128(kst + (q >> 1) * kTreeSlab + tid * 128 + (((4 * (q & 1) + j) ^ (tid & 7)) << 4), x[j]);
   }
 }
 
@@ -320,20 +321,22 @@ __device__ __forceinline__ void tail_v(const TreeArgs &a, TreeRec &r, uint32_t v
   }
 }
 
-template <int MT, bool kF16, bool kV>
-__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t st, uint32_t c_s, int n) {
+// Both groups run the same code where they can (the instruction cache holds it
+// once): kv 0 makes K, 1 makes V.
+template <int MT, bool kF16>
+__device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t st, uint32_t c_s, int kv, int n) {
   const int tid = threadIdx.x & 127, lane = tid & 31;
-  uint64_t *full = kV ? sm.vfull : sm.kfull, *empty = kV ? sm.vempty : sm.kempty;
+  uint64_t *full = kv ? sm.vfull : sm.kfull, *empty = kv ? sm.vempty : sm.kempty;
   const bool small = a.bshift == 5;
   // the pieces: of FP16 rows both groups take all, of codes each its ring's
-  constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2, kFirst = !kF16 && kV ? kRing : 0;
-  int at = kFirst;
+  constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2;
+  const int first = !kF16 && kv ? kRing : 0;
+  int at = 0;
   uint32_t turn = 0;  // modulo 2
-  auto piece_full = [&]() { return tree_wait(sm, &sm.cfull[at], turn, a); };
   auto piece_done = [&]() {
-    warp_arrive(&sm.cempty[at], lane);
-    if (++at == kFirst + kRing) {
-      at = kFirst;
+    warp_arrive(&sm.cempty[first + at], lane);
+    if (++at == kRing) {
+      at = 0;
       turn ^= 1;
     }
   };
@@ -342,11 +345,18 @@ __device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm
   // banks of both the piece and (as neighbouring rows of different slabs) the
   // operand
   const int hi = (tid >> 2) & 1, key = 2 * (tid >> 4) + hi, ch16 = (tid & 3) + 4 * (hi ^ ((tid >> 3) & 1));
-  const uint32_t k_to = (ch16 >> 2) * kTreeSlab + key * 128 + (((2 * (ch16 & 3)) ^ (key & 7)) << 4);
   // V: channel tid / 4 and 32, 64, 96 more, 16-slot chunk position tid % 4 of a
   // 64-token tile; eight lanes are two channels of four chunks
   const int v_ch = tid >> 2, v_pos = tid & 3;
+  // INT8: where the thread's 16 codes are in a piece, and go in the operand
+  // (the next: 2048 bytes on, and a quarter of the piece's part of the operand:
+  // 64 keys of K, 64 columns of V)
+  const uint32_t from8 = kv ? tid * 16 : key * 128 + ch16 * 16;
+  const uint32_t to8 = kv ? v_ch * 128 + (((2 * (v_pos ^ (v_ch >> 1 & 3))) ^ (v_ch & 7)) << 4)
+                          : (ch16 >> 2) * kTreeSlab + key * 128 + (((2 * (ch16 & 3)) ^ (key & 7)) << 4);
+  const uint32_t part = kv ? kTreeSlab : kTreeSlab / 2;
 
+#pragma unroll 1
   for (int j = 0; j < n; j++) {
     const int s = j & (kTreeStages - 1);
     const uint32_t ph = (j / kTreeStages) & 1, to = st + s * kTreeOperand;
@@ -359,97 +369,70 @@ __device__ __forceinline__ void tree_produce(const TreeArgs &a, TreeSmem<MT> &sm
     const uint32_t fmt = r.fmt;
     if (!tree_wait(sm, &empty[s], ph ^ 1, a)) return;
     if (!cold) {
-      if constexpr (kV) tail_v(a, r, to, tid);
+      if (kv) tail_v(a, r, to, tid);
       else tail_k(a, r, to, tid);
-    } else if constexpr (kF16) {
-      // pieces of 16 rows of K and V
+    } else {
+      // FP16: pieces of 16 rows of K and V.  Codes: two pieces of two units; of
+      // V with 32-token blocks four of one.
+      const int pieces = kF16 ? 8 : kv && small ? 4 : 2;
 #pragma unroll 1
-      for (int p = 0; p < 8; p++) {
-        if (!piece_full()) return;
-        const uint32_t c = c_s + at * kPiece;
-        if constexpr (kV) {
-          const int pair = tid & 63, rows = 8 * (tid >> 6);
-          const uint32_t ok = r.ok[p >> 1] >> (16 * (p & 1) + rows);
-          uint32_t w[8];
+      for (int p = 0; p < pieces; p++) {
+        if (!tree_wait(sm, &sm.cfull[first + at], turn, a)) return;
+        const uint32_t c = c_s + (first + at) * kPiece;
+        if constexpr (kF16) {
+          if (kv) {
+            const int pair = tid & 63, rows = 8 * (tid >> 6);
+            const uint32_t ok = r.ok[p >> 1] >> (16 * (p & 1) + rows);
+            uint32_t w[8];
 #pragma unroll
-          for (int k = 0; k < 8; k++) w[k] = lds32(c + (rows + k) * 512 + 256 + 4 * pair);
+            for (int k = 0; k < 8; k++) w[k] = lds32(c + (rows + k) * 512 + 256 + 4 * pair);
 #pragma unroll
-          for (int k = 0; k < 8; k++)  // (keys that are not there may hold anything)
-            if (!(ok >> k & 1)) w[k] = 0;
-          put_v(to, pair, 16 * p + rows, w);
-        } else {
+            for (int k = 0; k < 8; k++)  // (keys that are not there may hold anything)
+              if (!(ok >> k & 1)) w[k] = 0;
+            put_v(to, pair, 16 * p + rows, w);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
-            const int row = (tid >> 4) + 8 * i, c16 = tid & 15;
-            sts128(to + (c16 >> 3) * kTreeSlab + (16 * p + row) * 128 + (((c16 & 7) ^ (row & 7)) << 4),
-                   lds128(c + row * 512 + c16 * 16));
+            for (int i = 0; i < 2; i++) {
+              const int row = (tid >> 4) + 8 * i, c16 = tid & 15;
+              sts128(to + (c16 >> 3) * kTreeSlab + (16 * p + row) * 128 + (((c16 & 7) ^ (row & 7)) << 4),
+                     lds128(c + row * 512 + c16 * 16));
+            }
           }
-        }
-        piece_done();
-      }
-    } else if constexpr (!kV) {
-      // two pieces of two units
-#pragma unroll 1
-      for (int p = 0; p < 2; p++) {
-        if (!piece_full()) return;
-        const uint32_t c = c_s + at * kPiece;
-        if ((fmt & 15) == 0) {
+        } else if ((fmt & 15) == 0 && pieces == 2) {
           const TreeCodec f(false);
           uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; k++) x[k] = lds128(c + key * 128 + ch16 * 16 + 2048 * k);
+          for (int k = 0; k < 4; k++) x[k] = lds128(c + from8 + 2048 * k);
 #pragma unroll
-          for (int k = 0; k < 4; k++) put16(f, x[k], to + k_to + 8192 * p + 2048 * k);
+          for (int k = 0; k < 4; k++) put16(f, x[k], to + to8 + p * part + (k * part >> 2));
         } else {
 #pragma unroll 1
           for (int i = 0; i < 4; i++) {
-            const bool int4 = fmt >> (2 * p + i / 2) & 1;
-            const int k = key + 16 * (i & 1);
-            put16(TreeCodec(int4), get16(int4, c + 4096 * (i / 2) + (int4 ? k * 64 + ch16 * 8 : k * 128 + ch16 * 16)),
-                  to + k_to + 8192 * p + 2048 * i);
+            uint32_t from, dst;
+            bool int4, there = true;
+            if (!kv) {
+              int4 = fmt >> (2 * p + i / 2) & 1;
+              from = 4096 * (i / 2) + (key + 16 * (i & 1)) * (int4 ? 64 : 128) + ch16 * (int4 ? 8 : 16);
+              dst = to8 + p * part + i * (part >> 2);
+            } else {
+              // 64-slot tiles of a pair of units, or (32-token blocks) of one,
+              // whose slots 0..31 are its tokens
+              int4 = fmt >> (small ? p : 2 * p) & 1;
+              const int ch = v_ch + 32 * i, chunk = v_pos ^ (ch >> (int4 ? 2 : 1) & 3);  // slots 16 chunk ..
+              const int c8 = small ? 4 * (p & 1) + 2 * chunk : 2 * chunk;
+              there = !small || chunk < 2;
+              from = int4 ? ch * 32 + v_pos * 8 : ch * 64 + v_pos * 16;
+              dst = (small ? p >> 1 : p) * kTreeSlab + ch * 128 + ((c8 ^ (ch & 7)) << 4);
+            }
+            if (there) put16(TreeCodec(int4), get16(int4, c + from), to + dst);
           }
         }
         piece_done();
-      }
-    } else {
-      if ((fmt & 15) == 0 && !small) {
-        const TreeCodec f(false);
-        const uint32_t v_to = v_ch * 128 + (((2 * (v_pos ^ (v_ch >> 1 & 3))) ^ (v_ch & 7)) << 4);
-#pragma unroll 1
-        for (int p = 0; p < 2; p++) {
-          if (!piece_full()) return;
-          const uint32_t c = c_s + at * kPiece;
-          uint4 x[4];
-#pragma unroll
-          for (int k = 0; k < 4; k++) x[k] = lds128(c + tid * 16 + 2048 * k);
-#pragma unroll
-          for (int k = 0; k < 4; k++) put16(f, x[k], to + v_to + p * kTreeSlab + 4096 * k);
-          piece_done();
-        }
-      } else {
-        // 64-slot tiles of a pair of units, or (32-token blocks) of one, whose
-        // slots 0..31 are its tokens
-#pragma unroll 1
-        for (int p = 0; p < (small ? 4 : 2); p++) {
-          if (!piece_full()) return;
-          const uint32_t c = c_s + at * kPiece;
-          const bool int4 = fmt >> (small ? p : 2 * p) & 1;
-          const TreeCodec f(int4);
-#pragma unroll 1
-          for (int k = 0; k < 4; k++) {
-            const int ch = v_ch + 32 * k, chunk = v_pos ^ (ch >> (int4 ? 2 : 1) & 3);  // slots 16 chunk ..
-            const int c8 = small ? 4 * (p & 1) + 2 * chunk : 2 * chunk;
-            if (!small || chunk < 2)
-              put16(f, get16(int4, c + (int4 ? ch * 32 + v_pos * 8 : ch * 64 + v_pos * 16)),
-                    to + (small ? p >> 1 : p) * kTreeSlab + ch * 128 + ((c8 ^ (ch & 7)) << 4));
-          }
-          piece_done();
-        }
       }
     }
     warp_arrive(&full[s], lane);
     // the record is ready for the softmax: with V's part of a tail tile
-    if (kV == !cold && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
+    if (kv == !cold && lane == 0) mbar_arrive(&sm.mfull[j & (kTreeRecs - 1)]);
   }
 }
 
@@ -472,16 +455,9 @@ __device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, u
   constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2;
   const uint64_t policy = l2_policy_evict_first();
   const bool small = a.bshift == 5;
-  int at[2] = {0, 0}, sent[2] = {0, 0};  // by ring
-  uint32_t turn[2] = {0, 0};
-  auto room = [&](int ring) { return tree_wait<true>(sm, &sm.cempty[ring * kRing + at[ring]], turn[ring] ^ 1, a); };
-  auto next = [&](int ring) {
-    sent[ring]++;
-    if (++at[ring] == kRing) {
-      at[ring] = 0;
-      turn[ring] ^= 1;
-    }
-  };
+  // by ring: the next piece and its turn, in one number
+  uint32_t at0 = 0, at1 = 0;
+  auto next = [&](uint32_t at) { return (at & 15) + 1 == kRing ? (at & 16) ^ 16 : at + 1; };
   bool ok = true;
   for (int j = 0; j < n && ok; j++) {
     if (j % kTreeBatch == 0) {
@@ -494,56 +470,54 @@ __device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, u
     if constexpr (kF16) {
 #pragma unroll 1
       for (int p = 0; p < 8 && ok; p++) {
-        ok = room(0);
+        const int piece = at0 & 15;
+        ok = tree_wait<true>(sm, &sm.cempty[piece], at0 >> 4 ^ 1, a);
         if (!ok) break;
         const uint8_t *src = r.at[p >> 1];
-        uint64_t *bar = &sm.cfull[at[0]];
+        uint64_t *bar = &sm.cfull[piece];
         mbar_arrive_expect_tx(bar, src ? kPiece : 0);
-        if (src) bulk_to(c_s + at[0] * kPiece, src + (p & 1) * kPiece, kPiece, bar, policy);
-        next(0);
+        if (src) bulk_to(c_s + piece * kPiece, src + (p & 1) * kPiece, kPiece, bar, policy);
+        at0 = next(at0);
       }
     } else {
+      // pieces of K, then of V: units u and u + 1
 #pragma unroll 1
-      for (int u = 0; u < 4 && ok; u += 2) {
-        ok = room(0);
+      for (int p = 0; p < (small ? 6 : 4); p++) {
+        const int ring = p >> 1 ? 1 : 0, u = ring && small ? p - 2 : 2 * (p & 1);
+        const uint32_t at = ring ? at1 : at0;
+        const int piece = (ring ? kRing : 0) + (at & 15);
+        ok = tree_wait<true>(sm, &sm.cempty[piece], at >> 4 ^ 1, a);
         if (!ok) break;
-        const uint8_t *p0 = r.at[u], *p1 = r.at[u + 1];
-        const uint32_t n0 = !p0 ? 0 : fmt >> u & 1 ? 2048 : 4096, n1 = !p1 ? 0 : fmt >> (u + 1) & 1 ? 2048 : 4096;
-        uint64_t *bar = &sm.cfull[at[0]];
-        const uint32_t to = c_s + at[0] * kPiece;
-        mbar_arrive_expect_tx(bar, n0 + n1);
-        if (p0 == p1 && n0 == 4096) {  // the two halves of an INT8 tile are one run
-          bulk_to(to, p0, kPiece, bar, policy);
+        const uint8_t *p0 = r.at[u], *p1 = r.at[u + 1 & 3];
+        const uint32_t f = fmt >> u, to = c_s + piece * kPiece;
+        uint32_t n0 = f & 1 ? 2048 : 4096, n1 = f & 2 ? 2048 : 4096;
+        if (ring) {  // the whole V tile
+          p0 = p0 ? p0 + kTileBytes : p0;
+          n0 *= 2;
+          p1 = nullptr;
+        } else if (p0 == p1 && n0 == 4096) {  // the two halves of an INT8 tile are one run
+          n0 = kPiece;
+          p1 = nullptr;
         } else {
-          if (n0) bulk_to(to, p0 + (fmt >> (4 + u) & 1 ? n0 : 0), n0, bar, policy);
-          if (n1) bulk_to(to + 4096, p1 + (fmt >> (5 + u) & 1 ? n1 : 0), n1, bar, policy);
+          if (f & 16) p0 += n0;
+          if (f & 32) p1 += n1;
         }
-        next(0);
-      }
-#pragma unroll 1
-      for (int t = 0; t < (small ? 4 : 2) && ok; t++) {
-        ok = room(1);
-        if (!ok) break;
-        const int u = small ? t : 2 * t;
-        const uint8_t *src = r.at[u];
-        const uint32_t bytes = !src ? 0 : fmt >> u & 1 ? kTileBytes / 2 : kTileBytes;
-        uint64_t *bar = &sm.cfull[kRing + at[1]];
-        mbar_arrive_expect_tx(bar, bytes);
-        if (src) bulk_to(c_s + (kRing + at[1]) * kPiece, src + kTileBytes, bytes, bar, policy);
-        next(1);
+        uint64_t *bar = &sm.cfull[piece];
+        n0 = p0 ? n0 : 0;
+        n1 = p1 ? n1 : 0;
+        mbar_arrive_expect_tx(bar, n0 + n1);
+        if (n0) bulk_to(to, p0, n0, bar, policy);
+        if (n1) bulk_to(to + 4096, p1, n1, bar, policy);
+        (ring ? at1 : at0) = next(at);
       }
     }
   }
   // the copies in flight land before the CTA ends, also when nobody takes them
-#pragma unroll
-  for (int ring = 0; ring < (kF16 ? 1 : 2); ring++) {
-    for (int i = 0; i < kRing && i < sent[ring]; i++) {
-      if (--at[ring] < 0) {
-        at[ring] = kRing - 1;
-        turn[ring] ^= 1;
-      }
-      mbar_wait_bounded(&sm.cfull[ring * kRing + at[ring]], turn[ring], kDefaultWaitCycles);
-    }
+  // (a piece never used has its barrier's first phase to go: parity 1 is done)
+#pragma unroll 1
+  for (uint32_t i = 0; i < (kF16 ? 1 : 2) * kRing; i++) {
+    const uint32_t at = i < kRing ? at0 : at1;
+    mbar_wait_bounded(&sm.cfull[i], at >> 4 ^ ((i < kRing ? i : i - kRing) < (at & 15) ? 0 : 1), kDefaultWaitCycles);
   }
 }
 
@@ -690,20 +664,20 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
 // its halves of 64 keys the streams'.  MT 2: S of stream i at 128 i.  The weights
 // (FP16) replace the first half of the stream's columns of S.
 
-// (Half of a product's steps unrolled: instructions that fit the caches near the
-// SM count for more than the loops' overhead.)
+// (Four steps at a time: all eight do not pay for their code.)
 __device__ __forceinline__ void issue_qk(uint32_t t_s, uint32_t q, uint32_t q_slab, uint32_t k) {
-  uint64_t dq = tc_desc_sw128(q), dk = tc_desc_sw128(k);
-#pragma unroll 1
-  for (int h = 0; h < 2; h++, dq += q_slab >> 4, dk += kTreeSlab >> 4) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) tc_mma_ss(t_s, dq + 2 * i, dk + 2 * i, tc_idesc_f16(128), h > 0 || i > 0);
+  uint32_t dq = tc_desc_low(q), dk = tc_desc_low(k);
+#pragma unroll 4
+  for (int i = 0; i < 8; i++) {
+    tc_mma_ss(t_s, dq, dk, tc_idesc_f16(128), i > 0);
+    dq += i == 3 ? (q_slab >> 4) - 6 : 2;
+    dk += i == 3 ? (kTreeSlab >> 4) - 6 : 2;
   }
 }
 
 // 64 keys
 __device__ __forceinline__ void issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v, bool first) {
-  const uint64_t dv = tc_desc_sw128(v);
+  const uint32_t dv = tc_desc_low(v);
 #pragma unroll
   for (int i = 0; i < 4; i++) tc_mma_ts(t_o, t_p + 8 * i, dv + 2 * i, tc_idesc_f16(128), !first || i > 0);
 }
@@ -1200,8 +1174,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     tree_softmax<MT>(a, sm, tmem, n_tiles);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeProdRegs));
-    if (warp < kTreeSoft + kTreeProd / 2) tree_produce<MT, kF16, false>(a, sm, k_s, c_s, n_tiles);
-    else tree_produce<MT, kF16, true>(a, sm, v_s, c_s, n_tiles);
+    const int kv = (warp - kTreeSoft) / (kTreeProd / 2);
+    tree_produce<MT, kF16>(a, sm, kv ? v_s : k_s, c_s, kv, n_tiles);
   } else if (warp < kScoutWarp) {
     const int i = warp - kMmaWarp;
     if constexpr (MT == 2) tree_mma2(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);

@@ -446,79 +446,79 @@ __device__ __forceinline__ void bulk_to(uint32_t dst, const void *src, uint32_t 
       : "memory");
 }
 
-// One thread brings the bytes of the cold tiles: per tile K of two units (4096
-// bytes apart) and of the other two to one ring, their V tiles (32-token blocks:
-// one per unit) to the other; FP16 rows 16 at a time to one ring.  It alone
-// waits here, so its waits need no vote.
+// Lane i of one warp fills piece i of the rings, over and over, as soon as it is
+// free: per tile K of two units (4096 bytes apart) and of the other two in one
+// ring, their V tiles (32-token blocks: one per unit) in the other; FP16 rows 16
+// at a time in one ring.  Side by side, as a single thread takes longer to
+// issue a copy (about 900 cycles with all it looks up) than the copies last.
 template <int MT, bool kF16>
-__device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t c_s, int n) {
+__device__ __forceinline__ void tree_copy(const TreeArgs &a, TreeSmem<MT> &sm, uint32_t c_s, int n, int piece) {
   constexpr int kRing = kF16 ? TreeSmem<MT>::kPieces : TreeSmem<MT>::kPieces / 2;
   const uint64_t policy = l2_policy_evict_first();
-  const bool small = a.bshift == 5;
-  // by ring: the next piece and its turn, in one number
-  uint32_t at0 = 0, at1 = 0;
-  auto next = [&](uint32_t at) { return (at & 15) + 1 == kRing ? (at & 16) ^ 16 : at + 1; };
-  bool ok = true;
-  for (int j = 0; j < n && ok; j++) {
-    if (j % kTreeBatch == 0) {
-      const int batch = j / kTreeBatch;
-      if (!tree_wait<true>(sm, &sm.rfull[batch & 1], (batch >> 1) & 1, a)) break;
-    }
+  const bool is_v = piece >= kRing, small = a.bshift == 5;
+  const int pieces = kF16 ? 8 : is_v && small ? 4 : 2;  // of the ring per tile
+  const uint32_t to = c_s + piece * kPiece;
+  uint64_t *full = &sm.cfull[piece], *empty = &sm.cempty[piece];
+  int j = 0, p = is_v ? piece - kRing : piece;  // the tile and its piece to bring next
+  uint32_t turn = 0, t0 = 0;                    // modulo 2; when the lane began to wait
+#pragma unroll 1
+  while (j < n) {
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
-    if (!(r.flags & kTileCold)) continue;
-    const uint32_t fmt = r.fmt;
-    if constexpr (kF16) {
-#pragma unroll 1
-      for (int p = 0; p < 8 && ok; p++) {
-        const int piece = at0 & 15;
-        ok = tree_wait<true>(sm, &sm.cempty[piece], at0 >> 4 ^ 1, a);
-        if (!ok) break;
-        const uint8_t *src = r.at[p >> 1];
-        uint64_t *bar = &sm.cfull[piece];
-        mbar_arrive_expect_tx(bar, src ? kPiece : 0);
-        if (src) bulk_to(c_s + piece * kPiece, src + (p & 1) * kPiece, kPiece, bar, policy);
-        at0 = next(at0);
-      }
-    } else {
-      // pieces of K, then of V: units u and u + 1
-#pragma unroll 1
-      for (int p = 0; p < (small ? 6 : 4); p++) {
-        const int ring = p >> 1 ? 1 : 0, u = ring && small ? p - 2 : 2 * (p & 1);
-        const uint32_t at = ring ? at1 : at0;
-        const int piece = (ring ? kRing : 0) + (at & 15);
-        ok = tree_wait<true>(sm, &sm.cempty[piece], at >> 4 ^ 1, a);
-        if (!ok) break;
-        const uint8_t *p0 = r.at[u], *p1 = r.at[u + 1 & 3];
-        const uint32_t f = fmt >> u, to = c_s + piece * kPiece;
-        uint32_t n0 = f & 1 ? 2048 : 4096, n1 = f & 2 ? 2048 : 4096;
-        if (ring) {  // the whole V tile
-          p0 = p0 ? p0 + kTileBytes : p0;
-          n0 *= 2;
-          p1 = nullptr;
-        } else if (p0 == p1 && n0 == 4096) {  // the two halves of an INT8 tile are one run
-          n0 = kPiece;
-          p1 = nullptr;
-        } else {
-          if (f & 16) p0 += n0;
-          if (f & 32) p1 += n1;
+    const int batch = j / kTreeBatch;
+    bool ready = mbar_test_wait(&sm.rfull[batch & 1], (batch >> 1) & 1);
+    const bool skip = ready && (p >= pieces || !(r.flags & kTileCold));
+    ready = ready && !skip && mbar_test_wait(empty, turn ^ 1);
+    if (skip) {
+      if (r.flags & kTileCold) p -= pieces;
+      if (++j % kTreeBatch == 0) mbar_arrive(&sm.rfree[batch & 1]);
+    }
+    if (ready) {
+      const uint8_t *src, *src1 = nullptr;
+      uint32_t bytes, bytes1 = 0;
+      if constexpr (kF16) {
+        src = r.at[p >> 1];
+        bytes = src ? kPiece : 0;
+        src += (p & 1) * kPiece;
+      } else {
+        const int u = pieces == 4 ? p : 2 * p;
+        const uint32_t f = r.fmt >> u;
+        src = r.at[u];
+        bytes = !src ? 0 : f & 1 ? 2048 : 4096;
+        if (is_v) {  // the whole V tile
+          src += kTileBytes;
+          bytes *= 2;
+        } else {     // K of units u and u + 1
+          src1 = r.at[u + 1];
+          bytes1 = !src1 ? 0 : f & 2 ? 2048 : 4096;
+          if (src == src1 && bytes == 4096) {  // the two halves of an INT8 tile are one run
+            bytes = kPiece;
+            bytes1 = 0;
+          } else {
+            if (f & 16) src += bytes;
+            if (f & 32) src1 += bytes1;
+          }
         }
-        uint64_t *bar = &sm.cfull[piece];
-        n0 = p0 ? n0 : 0;
-        n1 = p1 ? n1 : 0;
-        mbar_arrive_expect_tx(bar, n0 + n1);
-        if (n0) bulk_to(to, p0, n0, bar, policy);
-        if (n1) bulk_to(to + 4096, p1, n1, bar, policy);
-        (ring ? at1 : at0) = next(at);
+      }
+      mbar_arrive_expect_tx(full, bytes + bytes1);
+      if (bytes) bulk_to(to, src, bytes, full, policy);
+      if (!kF16 && bytes1) bulk_to(to + 4096, src1, bytes1, full, policy);
+      p += kRing;
+      turn ^= 1;
+    }
+    if (ready || skip) {
+      t0 = 0;
+    } else {
+      const uint32_t t = static_cast<uint32_t>(clock()) | 1;
+      if (t0 == 0) t0 = t;
+      if (sm.abort || t - t0 > a.wait_cycles) {
+        sm.abort = 1;
+        break;
       }
     }
   }
   // the copies in flight land before the CTA ends, also when nobody takes them
-  // (a piece never used has its barrier's first phase to go: parity 1 is done)
-#pragma unroll 1
-  for (uint32_t i = 0; i < (kF16 ? 1 : 2) * kRing; i++) {
-    const uint32_t at = i < kRing ? at0 : at1;
-    mbar_wait_bounded(&sm.cfull[i], at >> 4 ^ ((i < kRing ? i : i - kRing) < (at & 15) ? 0 : 1), kDefaultWaitCycles);
-  }
+  // (before the first copy nothing is in flight, and parity 1 is done)
+  mbar_wait_bounded(full, turn ^ 1, kDefaultWaitCycles);
 }
 
 // ---- the scout ----
@@ -682,56 +682,58 @@ __device__ __forceinline__ void issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v,
   for (int i = 0; i < 4; i++) tc_mma_ts(t_o, t_p + 8 * i, dv + 2 * i, tc_idesc_f16(128), !first || i > 0);
 }
 
-// MT 1: one warp, Q K^T of the next tile before P V of this one.
-__device__ __forceinline__ void tree_mma1(const TreeArgs &a, TreeSmem<1> &sm, uint32_t q_s, uint32_t k_s, uint32_t v_s,
-                                          uint32_t tmem, int n) {
-  uint32_t flags = 0;
+// MT 1: a warp for Q K^T and one for P V.
+__device__ __forceinline__ void tree_mma_qk(const TreeArgs &a, TreeSmem<1> &sm, uint32_t q_s, uint32_t k_s, uint32_t tmem,
+                                            int n) {
+#pragma unroll 1
+  for (int j = 0; j < n; j++) {
+    const int s = j & 1;
+    const uint32_t ph = (j >> 1) & 1;
+    if (!tree_wait(sm, &sm.kfull[s], ph, a)) return;
+    const uint32_t flags = sm.rec[j & (kTreeRecs - 1)].flags, seg = flags >> kTileSegShift & 3;
+    const int qb = a.q_bufs == 2 ? seg & 1 : 0;
+    if ((flags & kTileFirst) && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return;
+    // S replaces the weights of tile j - 2: their P V is done
+    if (!tree_wait(sm, &sm.vempty[s], ph ^ 1, a)) return;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    if (tc_elect()) {
+      issue_qk(tmem + 128 * s, q_s + qb * 256 * a.q_rows, a.q_rows * 128, k_s + s * kTreeOperand);
+      tc_commit(&sm.sfull[s]);
+      tc_commit(&sm.kempty[s]);
+      if (flags & kTileLast) tc_commit(&sm.qempty[qb]);
+      if ((j + 1) % kTreeBatch == 0) mbar_arrive(&sm.rfree[(j / kTreeBatch) & 1]);
+    }
+    __syncwarp();
+  }
+}
+
+__device__ __forceinline__ void tree_mma_pv(const TreeArgs &a, TreeSmem<1> &sm, uint32_t v_s, uint32_t tmem, int n) {
   int begun = 0;  // segments
 #pragma unroll 1
-  for (int j = 0; j <= n; j++) {
-    uint32_t next = 0;
-    if (j < n) {
-      const int s = j & 1;
-      if (!tree_wait(sm, &sm.kfull[s], (j >> 1) & 1, a)) return;
-      next = sm.rec[j & (kTreeRecs - 1)].flags;
-      const uint32_t seg = next >> kTileSegShift & 3;
-      const int qb = a.q_bufs == 2 ? seg & 1 : 0;
-      if ((next & kTileFirst) && !tree_wait(sm, &sm.qfull[qb], (a.q_bufs == 2 ? seg >> 1 : seg) & 1, a)) return;
+  for (int j = 0; j < n; j++) {
+    const int s = j & 1;
+    const uint32_t ph = (j >> 1) & 1;
+    if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
+    const uint32_t flags = sm.rec[j & (kTreeRecs - 1)].flags;
+    const bool first = flags & kTileFirst;
+#pragma unroll 1
+    for (int i = 0; i < 2; i++) {
+      if (first && !tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
+      if (!tree_wait(sm, &sm.pfull[i][s], ph, a)) return;
       fence_proxy_async_smem();
       tc_fence_after();
-      // (S replaces the weights of tile j - 2, whose P V is issued)
       if (tc_elect()) {
-        issue_qk(tmem + 128 * s, q_s + qb * 256 * a.q_rows, a.q_rows * 128, k_s + s * kTreeOperand);
-        tc_commit(&sm.sfull[s]);
-        tc_commit(&sm.kempty[s]);
-        if (next & kTileLast) tc_commit(&sm.qempty[qb]);
+        issue_pv(tmem + 256 + 128 * i, tmem + 128 * s + 64 * i, v_s + s * kTreeOperand + i * kTreeSlab, first);
+        if (flags & kTileLast) tc_commit(&sm.odone[i]);
+        if (i == 1) {
+          tc_commit(&sm.vempty[s]);
+          if ((j + 1) % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch) & 1]);
+        }
       }
       __syncwarp();
     }
-    if (j > 0) {
-      const int s = (j - 1) & 1;
-      const uint32_t ph = ((j - 1) >> 1) & 1;
-      const bool first = flags & kTileFirst;
-      if (!tree_wait(sm, &sm.vfull[s], ph, a)) return;
-#pragma unroll 1
-      for (int i = 0; i < 2; i++) {
-        if (first && !tree_wait(sm, &sm.ofree[i], (begun & 1) ^ 1, a)) return;
-        if (!tree_wait(sm, &sm.pfull[i][s], ph, a)) return;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        if (tc_elect()) {
-          issue_pv(tmem + 256 + 128 * i, tmem + 128 * s + 64 * i, v_s + s * kTreeOperand + i * kTreeSlab, first);
-          if (flags & kTileLast) tc_commit(&sm.odone[i]);
-          if (i == 1) {
-            tc_commit(&sm.vempty[s]);
-            if (j % kTreeBatch == 0) tc_commit(&sm.rfree[(j / kTreeBatch - 1) & 1]);
-          }
-        }
-        __syncwarp();
-      }
-      if (first) begun++;
-    }
-    flags = next;
+    if (first) begun++;
   }
 }
 
@@ -1117,7 +1119,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       mbar_init(&sm.kempty[i], MT);
       mbar_init(&sm.vempty[i], MT);
       mbar_init(&sm.rfull[i], 1);
-      mbar_init(&sm.rfree[i], MT);
+      mbar_init(&sm.rfree[i], kTreeMma + TreeSmem<MT>::kPieces);
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.pfull[i][0], 4);
       mbar_init(&sm.pfull[i][1], 4);
@@ -1179,7 +1181,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   } else if (warp < kScoutWarp) {
     const int i = warp - kMmaWarp;
     if constexpr (MT == 2) tree_mma2(a, sm, q_s, k_s, v_s, tmem, n_tiles, i);
-    else if (i == 0) tree_mma1(a, sm, q_s, k_s, v_s, tmem, n_tiles);
+    else if (i == 0) tree_mma_qk(a, sm, q_s, k_s, tmem, n_tiles);
+    else tree_mma_pv(a, sm, v_s, tmem, n_tiles);
     __syncwarp();
     // no MMA is in flight when TMEM is given back
     if (tc_elect()) tc_commit(&sm.drain[i]);
@@ -1187,7 +1190,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     if (!mbar_wait_bounded(&sm.drain[i], 0, kDefaultWaitCycles)) sm.abort = 1;
     __syncwarp();
   } else if (warp > kScoutWarp) {
-    if (lane == 0) tree_copy<MT, kF16>(a, sm, c_s, n_tiles);
+    if (lane < TreeSmem<MT>::kPieces) tree_copy<MT, kF16>(a, sm, c_s, n_tiles, lane);
     __syncwarp();
   } else {
     tree_scout<MT, kF16>(a, sm, q_s, n_tiles);

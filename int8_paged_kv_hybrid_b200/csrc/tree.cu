@@ -53,7 +53,7 @@ constexpr float kLagScale = 256.f;
 // launch; the softmax warps take what the producers do not need.
 constexpr int kTreeSoft = 8, kTreeProd = 8, kTreeMma = 2;
 constexpr int kTreeThreads = 32 * (kTreeSoft + kTreeProd + kTreeMma + 2);
-constexpr int kTreeSoftRegs = 112, kTreeProdRegs = 80;
+constexpr int kTreeSoftRegs = 120, kTreeProdRegs = 72;
 
 // TreeRec::flags: the first and the last tile of its segment (the part of a unit
 // that this CTA has); every key attended by every row and no
@@ -956,39 +956,58 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         return true;
       };
       uint64_t sum0 = 0, sum1 = 0;
-      // S by units of 32 keys, twice: for the maximum and for the weights
       constexpr int kUnits = MT == 1 ? 2 : 4;
       const int u0 = MT == 1 ? 2 * stream : 0;
       const uint32_t t_p = t_s + 32 * u0;
-      float top = -INFINITY;
+      if (!plain) {
+        // some keys are masked (or a scale is negative): the logits, -inf where
+        // masked, replace S
 #pragma unroll 1
-      for (int u = 0; u < kUnits; u++) {
-        uint32_t v[32];
-        tc_ld32(t_p + 32 * u, v);
-        float scale = r.k_scale[u0 + u] * a.qk_scale;
-        tc_wait_ld(v);
-        if (!plain) {
-          // some keys are masked (or the scale is negative): the logits, -inf
-          // where masked, replace S
-          uint32_t ok = r.ok[u0 + u];
-          if (tail) ok |= tree_nodes(r, u0 + u, r.row0 - r.hot + 32 * (u0 + u), nodes, odd);
+        for (int u = u0; u < u0 + kUnits; u++) {
+          uint32_t v[32];
+          tc_ld32(t_s + 32 * u, v);
+          const float scale = r.k_scale[u] * a.qk_scale;
+          uint32_t ok = r.ok[u];
+          if (tail) ok |= tree_nodes(r, u, r.row0 - r.hot + 32 * u, nodes, odd);
+          tc_wait_ld(v);
 #pragma unroll
           for (int k = 0; k < 32; k++) v[k] = ok >> k & 1 ? __float_as_uint(__uint_as_float(v[k]) * scale) : 0xff800000u;
-          scale = 1.f;
-          tc_st32(t_p + 32 * u, v);
+          tc_st32(t_s + 32 * u, v);
         }
-        top = fmaxf(top, max_of<32>(v) * scale);
+        tc_wait_st();
       }
-      if (!plain) tc_wait_st();
-      if (!follow(top)) return;
-      const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+      auto k_scale = [&](int u) { return plain ? r.k_scale[u] * a.qk_scale : 1.f; };
+      // the maximum, then the weights, by units of 32 keys; MT 1 keeps its 64 logits
+      // in registers, MT 2 reads its 128 twice
+      if constexpr (MT == 1) {
+        uint32_t v[2][32];
+        tc_ld32(t_p, v[0]);
+        tc_ld32(t_p + 32, v[1]);
+        tc_wait_ld(v[0]);
+        tc_wait_ld(v[1]);
+        const float s0 = k_scale(u0), s1 = k_scale(u0 + 1);
+        if (!follow(fmaxf(max_of<32>(v[0]) * s0, max_of<32>(v[1]) * s1))) return;
+        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+        tree_weights(v[0], s0, r.v_scale[u0] * inv, minus_m, t_p, sum0, sum1);
+        tree_weights(v[1], s1, r.v_scale[u0 + 1] * inv, minus_m, t_p + 16, sum0, sum1);
+      } else {
+        float top = -INFINITY;
 #pragma unroll 1
-      for (int u = 0; u < kUnits; u++) {
-        uint32_t v[32];
-        tc_ld32(t_p + 32 * u, v);
-        const float scale = plain ? r.k_scale[u0 + u] * a.qk_scale : 1.f, factor = r.v_scale[u0 + u] * inv;
-        tc_wait_ld(v);
-        tree_weights(v, scale, factor, minus_m, t_p + 16 * u, sum0, sum1);
+        for (int u = 0; u < kUnits; u++) {
+          uint32_t v[32];
+          tc_ld32(t_s + 32 * u, v);
+          tc_wait_ld(v);
+          top = fmaxf(top, max_of<32>(v) * k_scale(u));
+        }
+        if (!follow(top)) return;
+        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+        for (int u = 0; u < kUnits; u++) {
+          uint32_t v[32];
+          tc_ld32(t_s + 32 * u, v);
+          tc_wait_ld(v);
+          tree_weights(v, k_scale(u), r.v_scale[u] * inv, minus_m, t_s + 16 * u, sum0, sum1);
+        }
       }
       float x, y;
       unpack2(add2(sum0, sum1), x, y);

@@ -904,14 +904,24 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
 
   for (int j = 0; j < n; j++) {
     const int buf = MT == 1 ? j & 1 : stream;
-    if (!tree_wait(sm, &sm.sfull[buf], (MT == 1 ? j >> 1 : j) & 1, a)) return;
     if (!tree_wait(sm, &sm.mfull[j & (kTreeRecs - 1)], (j / kTreeRecs) & 1, a)) return;
-    tc_fence_after();
     const TreeRec &r = sm.rec[j & (kTreeRecs - 1)];
     const uint32_t flags = r.flags, t_s = lanes + 128 * buf;
     const bool first = flags & kTileFirst;
     const int row = r.mg * 128 * MT + part_row;  // of the sequence and kv head
     const bool live = row < r.rows, warp_live = row - lane < r.rows;
+    const float v_max = r.v_max;
+    float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;  // MT 1: the scales of the stream's two units
+    if (MT == 1) {
+      if (flags & kTilePlain) {
+        ks0 = r.k_scale[2 * stream] * a.qk_scale;
+        ks1 = r.k_scale[2 * stream + 1] * a.qk_scale;
+      }
+      vs0 = r.v_scale[2 * stream];
+      vs1 = r.v_scale[2 * stream + 1];
+    }
+    if (!tree_wait(sm, &sm.sfull[buf], (MT == 1 ? j >> 1 : j) & 1, a)) return;
+    tc_fence_after();
     if (first) {
       m = -INFINITY;
       l = 0.f;
@@ -928,7 +938,6 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       // m and r follow the maxima when they lag too far behind; O and l follow
       // them
       auto follow = [&](float top) -> bool {
-        const float v_max = r.v_max;
         float ref_new = first ? 1.f : ref;
         if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
         const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
@@ -985,11 +994,10 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         tc_ld32(t_p + 32, v[1]);
         tc_wait_ld(v[0]);
         tc_wait_ld(v[1]);
-        const float s0 = k_scale(u0), s1 = k_scale(u0 + 1);
-        if (!follow(fmaxf(max_of<32>(v[0]) * s0, max_of<32>(v[1]) * s1))) return;
+        if (!follow(fmaxf(max_of<32>(v[0]) * ks0, max_of<32>(v[1]) * ks1))) return;
         const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
-        tree_weights(v[0], s0, r.v_scale[u0] * inv, minus_m, t_p, sum0, sum1);
-        tree_weights(v[1], s1, r.v_scale[u0 + 1] * inv, minus_m, t_p + 16, sum0, sum1);
+        tree_weights(v[0], ks0, vs0 * inv, minus_m, t_p, sum0, sum1);
+        tree_weights(v[1], ks1, vs1 * inv, minus_m, t_p + 16, sum0, sum1);
       } else {
         float top = -INFINITY;
 #pragma unroll 1
@@ -1015,7 +1023,13 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       tc_wait_st();
     }
     // what the segment's end needs of the record, which may be gone after pfull
-    const int b = r.b, hk = r.hk, mg = r.mg, rest = r.rest;
+    int b = 0, hk = 0, mg = 0, rest = 0;
+    if (flags & kTileLast) {
+      b = r.b;
+      hk = r.hk;
+      mg = r.mg;
+      rest = r.rest;
+    }
     tc_fence_before();
     warp_arrive(&sm.pfull[stream][MT == 1 ? buf : 0], lane);
     if (!(flags & kTileLast)) continue;

@@ -314,3 +314,67 @@ def test_graph_replayed_after_growth_and_two_streams():
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i], out) and torch.equal(lses[i], lse)
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The kernel's bounded waits cut to a few cycles: the call ends, the status
+    says so, the cache is untouched, and a call with the default limit is right."""
+    w = synth.custom_workload("limit", [3000, 1200, 0, 700], 32, 8, seed=17, schedule="chunk")
+    cache, ora = make_pair(w)
+    replay(w, cache, ora)
+    for nodes in (8, 64):                      # one and two tiles of 128 rows per CTA
+        q, k, v = inputs(w, nodes, 2)
+        ws = cache.tree_workspace(nodes)
+        try:
+            _lib.hyb_set_wait_limit(4)
+            run(cache, q, k, v, None, None, w.softmax_scale, workspace=ws)
+        finally:
+            _lib.hyb_set_wait_limit(0)
+        assert cache.status(clear=True) == _lib.HYB_STATUS_TIMEOUT
+        got, lse = run(cache, q, k, v, None, None, w.softmax_scale, workspace=ws)
+        check(w, ora, got, lse, q, k, v, None, None, w.softmax_scale)
+        assert cache.status() == 0
+
+
+@pytest.mark.parametrize("batch,nodes", [(700, 3), (1500, 1)])
+def test_more_sequences_than_threads(batch, nodes):
+    """Short sequences, many of them without a node: units of one tile, several
+    sequences per thread in the search for a CTA's first tile."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 70, size=batch)
+    lens[::97] = 300
+    w = synth.custom_workload("many", [int(n) for n in lens], 4, 2, seed=5, schedule="one")
+    cache, ora = make_pair(w)
+    replay(w, cache, ora)
+    q, k, v = inputs(w, nodes, 3)
+    n_tree = rng.integers(0, nodes + 1, size=batch).astype(np.int32)
+    n_tree[100:400] = 0
+    n_tree[-1] = 0
+    got, lse = run(cache, q, k, v, None, n_tree, w.softmax_scale)
+    check(w, ora, got, lse, q, k, v, None, n_tree, w.softmax_scale)
+    assert cache.status() == 0
+
+
+def test_no_node_anywhere():
+    """n_tree 0 for every sequence: nothing is written."""
+    w = synth.custom_workload("none", [40, 200], 8, 2, seed=5)
+    cache, ora = make_pair(w)
+    replay(w, cache, ora)
+    q, k, v = inputs(w, 4, 3)
+    got, lse = run(cache, q, k, v, None, np.zeros(2, np.int32), w.softmax_scale)
+    assert (got == MARK).all() and (lse == MARK).all() and cache.status() == 0
+
+
+@pytest.mark.parametrize("bits,hot,block", [(8, 32, 64), (4, 16, 32), (0, 128, 128)])
+def test_two_row_tiles_with_short_trees(bits, hot, block):
+    """Room for 64 nodes of eight heads each (four tiles of 128 rows), trees of
+    one to some nodes: rows and whole row tiles without a query."""
+    w = synth.custom_workload("short", [0, 31, 500, 1030, 129, 77], 16, 2, seed=11, hot=hot, block=block, max_step=64)
+    cache, ora = make_pair(w, quant_bits=bits)
+    replay(w, cache, ora)
+    q, k, v = inputs(w, 64, 3)
+    mask = random_masks(np.random.default_rng(4), w.batch, 64, "any")
+    n_tree = np.array([1, 16, 17, 33, 64, 0], np.int32)
+    got, lse = run(cache, q, k, v, mask, n_tree, w.softmax_scale)
+    check(w, ora, got, lse, q, k, v, mask, n_tree, w.softmax_scale)
+    assert cache.status() == 0

@@ -23,16 +23,36 @@
 // tree_combine_kernel merges them in the order of the tiles.
 //
 // Inside a CTA (20 warps): a scout warp looks the tiles up (block table, scales,
-// segment ends) some tiles ahead, writes their records, starts their way into
-// L2 and fetches the query rows; a copy warp brings their bytes into a ring in
-// shared memory by bulk copies; four producer warps turn K, four V, from codes
-// or rows into FP16 in the 128-byte swizzled layout of the MMA's shared
-// operands; two groups of four softmax warps (one query row per thread) keep two
-// softmax streams and write the weights over the logits in TMEM, where the
-// second product reads them as its A operand.  The streams are the two row
-// tiles (MT 2, with an MMA warp each), or the two halves of every tile's keys
-// (MT 1), merged at a unit's end: then a tile's softmax is 64 keys per thread,
-// and S has two buffers, so that Q K^T of the next tile runs behind it.
+// segment ends) some tiles ahead, writes their records and fetches the query
+// rows; the lanes of a copy warp bring their bytes into rings in shared memory by
+// bulk copies; four producer warps turn K, four V, from codes or rows into FP16 in
+// the 128-byte swizzled layout of the MMA's shared operands; two MMA warps issue
+// the products; two groups of four softmax warps (one query row per thread) keep
+// two softmax streams and write the weights over the logits in TMEM, where the
+// second product reads them as its A operand.  The streams are the two row tiles
+// (MT 2, with an MMA warp each), or the two halves of every tile's keys (MT 1),
+// merged at a unit's end: then a tile's softmax is 64 keys per thread, and S has
+// two buffers, so that Q K^T of the next tile (one MMA warp) runs behind it and
+// P V of the last one (the other).
+//
+// What bounds it (measured with the L2 flushed, us; "long": 4 sequences of 32768
+// .. 131072 tokens, 32 nodes, 32 heads, 8 kv heads; "short trees": 64 sequences of
+// 256 .. 8192 tokens, 8 nodes; "wide": 8 of 16384 tokens, 64 nodes, 64 heads).  No
+// unit is busy most of the time: of long's 247 us the bytes need 101 and the
+// products 103.  The time goes to instructions: six roles on one SM, whose code
+// has to come from its instruction cache (with 110 KB of unrolled code 31% of the
+// requests missed and a stall for instructions was the commonest: long 372; as
+// loops, 86 KB: 285), and to the softmax warps' path from one tile to the next,
+// about 2600 cycles, of which the powers of two take 1120.  What was tried:
+//   a lane per ring piece issues the copies, instead of one thread: long 283 -> 261
+//   64 logits stay in registers between maximum and weights (MT 1): long 262 -> 247
+//   K and V producers share their code: short trees 354 -> 342
+//   120 / 72 registers for softmax / producers, not 112 / 80: short trees 330 -> 315
+//   four MMA steps per loop turn, not one: wide 450 -> 422
+//   a quarter of the powers of two by a polynomial: long 248 -> 252, not kept
+//   rings of two pieces instead of three: no difference
+// Where the rows fill a quarter of the tile or less (at most 32 rows), one
+// scheduler of the SM has all the softmax work, and the other three none.
 #include "kernels.cuh"
 #include "spec.cuh"
 #include "tc05.cuh"
@@ -222,9 +242,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
 // Sixteen codes, INT8 or (of eight bytes, code e of a word the low nibble of byte

@@ -151,6 +151,9 @@ struct TreeSeq {
   int status;
 };
 
+// ceil(tokens / 128), also where the sum with 127 would pass 32 bits
+__device__ __forceinline__ int tiles_of(int tokens) { return tokens / kTK + (tokens % kTK != 0); }
+
 template <int MT>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   TreeSeq s;
@@ -166,7 +169,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   s.cold = bad ? 0 : max(0, L - a.hot_tokens);
   s.hot = bad ? 0 : L - s.cold;
   s.keys = bad ? 0 : s.nt;
-  s.tiles = max(1, (s.cold + kTK - 1) / kTK + (s.hot + s.keys + kTK - 1) / kTK);
+  s.tiles = max(1, tiles_of(s.cold) + tiles_of(s.hot + s.keys));
   s.groups = (s.nt * a.group + 128 * MT - 1) / (128 * MT);
   return s;
 }
@@ -592,8 +595,9 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
     const int seg = segs + __popc(firsts & (0xffffffffu >> (31 - (4 * k)))) - 1;
     const int rows = q.nt * a.group;
 
-    const int p = t * kTK + 32 * c;  // the unit's first position
-    const bool cold = t * kTK < q.cold;
+    const int cold_tiles = tiles_of(q.cold);
+    const bool cold = t < cold_tiles;
+    const int p = cold ? t * kTK + 32 * c : 0;  // the unit's first position
     int valid = cold ? max(0, min(32, q.cold - p)) : 0;
     const uint8_t *at = nullptr;
     float2 sc = make_float2(1.f, 1.f);
@@ -618,7 +622,7 @@ __device__ __forceinline__ void tree_scout(const TreeArgs &a, TreeSmem<MT> &sm, 
     }
     // (an empty unit has no say in the reference scale)
     if (!kF16 && cold && valid == 0) sc = make_float2(0.f, 0.f);
-    const int row0 = (t - (q.cold + kTK - 1) / kTK) * kTK;
+    const int row0 = (t - cold_tiles) * kTK;
     if (!cold) valid = max(0, min(32, q.hot - row0 - 32 * c));
     const uint32_t ok = valid >= 32 ? 0xffffffffu : (1u << valid) - 1;
     bool plain = valid >= 32 && sc.x * a.qk_scale >= 0.f;

@@ -921,6 +921,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
   // the row's state in the segment
   uint64_t odd = 0;  // attended nodes whose V is not finite
   float m = -INFINITY, l = 0.f, ref = 1.f;
+  float inv = 1.f, minus_m = 0.f;  // 1 / ref, -m (0 while m is -inf)
   int ends = 0;      // segments
 
   for (int j = 0; j < n; j++) {
@@ -959,10 +960,10 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       // m and r follow the maxima when they lag too far behind; O and l follow
       // them
       auto follow = [&](float top) -> bool {
-        float ref_new = first ? 1.f : ref;
-        if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
-        const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
-        if (__any_sync(0xffffffffu, m_new != m || ref_new != ref)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, first || top > m + kLagLog2 || v_max > kLagScale * ref), 0)) {
+          float ref_new = first ? 1.f : ref;
+          if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
+          const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
           if (!first) {
             // (MT 2: the stream's last P V is done, as this tile's S came after it)
             if (MT == 1 && !tree_wait(sm, &sm.vempty[(j - 1) & 1], ((j - 1) >> 1) & 1, a)) return false;
@@ -982,6 +983,8 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
           }
           m = m_new;
           ref = ref_new;
+          inv = __fdividef(1.f, ref);
+          minus_m = m == -INFINITY ? 0.f : -m;
         }
         return true;
       };
@@ -1016,7 +1019,6 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         tc_wait_ld(v[0]);
         tc_wait_ld(v[1]);
         if (!follow(fmaxf(max_of<32>(v[0]) * ks0, max_of<32>(v[1]) * ks1))) return;
-        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
         tree_weights(v[0], ks0, vs0 * inv, minus_m, t_p, sum0, sum1);
         tree_weights(v[1], ks1, vs1 * inv, minus_m, t_p + 16, sum0, sum1);
       } else {
@@ -1029,7 +1031,6 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
           top = fmaxf(top, max_of<32>(v) * k_scale(u));
         }
         if (!follow(top)) return;
-        const float inv = __fdividef(1.f, ref), minus_m = m == -INFINITY ? 0.f : -m;
 #pragma unroll 1
         for (int u = 0; u < kUnits; u++) {
           uint32_t v[32];

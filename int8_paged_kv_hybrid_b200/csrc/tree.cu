@@ -38,21 +38,24 @@
 // What bounds it (measured with the L2 flushed, us; "long": 4 sequences of 32768
 // .. 131072 tokens, 32 nodes, 32 heads, 8 kv heads; "short trees": 64 sequences of
 // 256 .. 8192 tokens, 8 nodes; "wide": 8 of 16384 tokens, 64 nodes, 64 heads).  No
-// unit is busy most of the time: of long's 247 us the bytes need 101 and the
+// unit is busy most of the time: of long's 241 us the bytes need 101 and the
 // products 103.  The time goes to instructions: six roles on one SM, whose code
 // has to come from its instruction cache (with 110 KB of unrolled code 31% of the
 // requests missed and a stall for instructions was the commonest: long 372; as
 // loops, 86 KB: 285), and to the softmax warps' path from one tile to the next,
-// about 2600 cycles, of which the powers of two take 1120.  What was tried:
+// about 2500 cycles, of which two warps' powers of two take 1120 and the waits,
+// records, the TMEM round trip and the arrival 1400 whatever the rows and keys
+// are.  What was tried:
 //   a lane per ring piece issues the copies, instead of one thread: long 283 -> 261
 //   64 logits stay in registers between maximum and weights (MT 1): long 262 -> 247
 //   K and V producers share their code: short trees 354 -> 342
 //   120 / 72 registers for softmax / producers, not 112 / 80: short trees 330 -> 315
 //   four MMA steps per loop turn, not one: wide 450 -> 422
+//   one test per tile whether maximum and reference may stay: long 248 -> 241
 //   a quarter of the powers of two by a polynomial: long 248 -> 252, not kept
-//   rings of two pieces instead of three: no difference
-// Where the rows fill a quarter of the tile or less (at most 32 rows), one
-// scheduler of the SM has all the softmax work, and the other three none.
+//   up to 64 rows twice in the tile, half the keys for each: short trees 289 -> 302
+//   (the fixed part stays, the second Q buffer goes), not kept
+//   rings of two pieces instead of three: codes the same, FP16 rows 85 -> 90
 #include "kernels.cuh"
 #include "spec.cuh"
 #include "tc05.cuh"

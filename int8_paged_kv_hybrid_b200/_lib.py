@@ -364,12 +364,35 @@ def need(ok, what):
         raise HybError(HYB_ERR_INVALID_VALUE, what)
 
 
-def on_device(device, stream, call):
+def on_device(device, stream, call, made=None):
     """call(stream) on `stream`, by default the current stream of `device`
-    (which need not be the current device)."""
+    (which need not be the current device).
+
+    `made` is a list where `call` makes buffers of its own.  `stream` is then the
+    current one inside `call`: what fills a buffer comes before the kernels that
+    use it, and the memory of one that is freed goes to later work of the same
+    stream only.  The buffers that the caller gets are put in `made`; their memory
+    also waits for the stream that was current at the caller."""
     import torch
     need(device.type == "cuda", "a call on %s buffers" % device)
+    if made is not None and stream is not None:
+        caller, s = torch.cuda.current_stream(device), _torch_stream(device, stream)
+        need(s.device == device, "a stream of %s for buffers on %s" % (s.device, device))
+        with torch.cuda.stream(s):
+            result = call(s)
+        for x in made:
+            x.record_stream(caller)
+        return result
     if device.index == torch.cuda.current_device():
         return call(torch.cuda.current_stream() if stream is None else stream)
     with torch.cuda.device(device):
         return call(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _torch_stream(device, stream):
+    """The torch stream of a stream or a raw handle (0 and 1: the default stream)."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)

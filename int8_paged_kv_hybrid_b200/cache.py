@@ -173,7 +173,9 @@ class HybridKVCache:
 
     def tree_decode(self, q, k_tree, v_tree, tree_mask, softmax_scale, n_tree=None, out=None, lse=None,
                     workspace=None, stream=None):
-        """Attention of drafted nodes (hyb_tree_attn): q FP16 CUDA
+        """Attention of drafted nodes (hyb_tree_attn) on `stream` (default: the
+        current one of the cache's device), where buffers not given are made too:
+        q FP16 CUDA
         [batch][nodes][Hq][128], k_tree / v_tree FP16 [batch][nodes][Hkv][128],
         tree_mask int64 [batch][nodes] (bit j: the node attends node j; see
         tree_masks) or None for a chain, n_tree int32 [batch] or None for all
@@ -182,24 +184,27 @@ class HybridKVCache:
         were (zero, and -inf, in an `out` and a `lse` that this call makes)."""
         import torch
         need, dev, nodes = _lib.need, self.device, q.shape[1] if q.dim() == 4 else 0
-        kv_shape = (self.batch, nodes, self.hkv, HEAD_DIM)
-        if out is None:
-            out = torch.zeros((self.batch, nodes, self.hq, HEAD_DIM), dtype=torch.float16, device=dev)
-        for name, x, shape in (("q", q, (self.batch, nodes, self.hq, HEAD_DIM)), ("k_tree", k_tree, kv_shape),
-                               ("v_tree", v_tree, kv_shape), ("out", out, (self.batch, nodes, self.hq, HEAD_DIM))):
+        q_shape, kv_shape = (self.batch, nodes, self.hq, HEAD_DIM), (self.batch, nodes, self.hkv, HEAD_DIM)
+        for name, x, shape in (("q", q, q_shape), ("k_tree", k_tree, kv_shape), ("v_tree", v_tree, kv_shape)):
             need(x.shape == shape and x.dtype == torch.float16 and x.device == dev and x.is_contiguous(),
                  "tree_decode: " + name)
-        for name, x, shape, dtype in (("tree_mask", tree_mask, (self.batch, nodes), torch.int64),
+        for name, x, shape, dtype in (("out", out, q_shape, torch.float16),
+                                      ("tree_mask", tree_mask, (self.batch, nodes), torch.int64),
                                       ("n_tree", n_tree, (self.batch,), torch.int32),
                                       ("lse", lse, (self.batch, nodes, self.hq), torch.float32)):
             need(x is None or (x.shape == shape and x.dtype == dtype and x.device == dev and x.is_contiguous()),
                  "tree_decode: " + name)
-        if workspace is None:
-            workspace = self.tree_workspace(nodes)
-        need(workspace.device == dev and workspace.is_contiguous(), "tree_decode: workspace")
-        _lib.on_device(dev, stream, lambda s: _lib.hyb_tree_attn(
-            self.desc, q, k_tree, v_tree, tree_mask, n_tree, nodes, softmax_scale, workspace, out, lse, s))
-        return out
+        need(workspace is None or (workspace.device == dev and workspace.is_contiguous()), "tree_decode: workspace")
+        made = []
+
+        def call(s):
+            ws = self.tree_workspace(nodes) if workspace is None else workspace
+            if out is None:
+                made.append(torch.zeros(q_shape, dtype=torch.float16, device=dev))
+            o = made[0] if out is None else out
+            _lib.hyb_tree_attn(self.desc, q, k_tree, v_tree, tree_mask, n_tree, nodes, softmax_scale, ws, o, lse, s)
+            return o
+        return _lib.on_device(dev, stream, call, made if out is None or workspace is None else None)
 
     def status(self, clear=False, stream=None):
         return _lib.hyb_read_status(self.desc, clear, stream)

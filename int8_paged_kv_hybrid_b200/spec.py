@@ -34,7 +34,9 @@ class BlockPool:
     by the sequences of a batch (hyb_pool_desc).  A new pool has every block
     free.  Existing buffers may be given: ring int32 [num_phys_blocks], state
     int32 [2] (head, count), n_blocks int32 [batch], block_table int32
-    [batch][max_blocks_per_seq].  `block_table` is what HybridKVCache takes."""
+    [batch][max_blocks_per_seq].  `block_table` is what HybridKVCache takes.
+    A call works on `stream` (default: the current one of the pool's device),
+    where the buffers that it is not given are made too."""
 
     def __init__(self, batch, num_phys_blocks, max_blocks_per_seq, hot_tokens=HOT, block_size=BLOCK, device="cuda",
                  ring=None, state=None, n_blocks=None, block_table=None, status_word=None):
@@ -83,11 +85,11 @@ class BlockPool:
         lens int32 CUDA [batch]; in place, or into the successor `to`."""
         self._check(lens, (self.batch,), "BlockPool.resize: lens")
         _lib.need(to is None or to.device == self.device, "BlockPool.resize: to")
-        if workspace is None:
-            workspace = self.workspace()
-        _lib.need(workspace.device == self.device and workspace.is_contiguous(), "BlockPool.resize: workspace")
+        _lib.need(workspace is None or (workspace.device == self.device and workspace.is_contiguous()),
+                  "BlockPool.resize: workspace")
         _lib.on_device(self.device, stream, lambda s: _lib.hyb_pool_resize(
-            self.desc, None if to is None else to.desc, lens, workspace, s))
+            self.desc, None if to is None else to.desc, lens, self.workspace() if workspace is None else workspace, s),
+            [] if workspace is None else None)
         return self if to is None else to
 
     def slot_map(self, lens, n_tok, max_total, first=None, cu=None, slots=None, stream=None):
@@ -97,18 +99,27 @@ class BlockPool:
         behind cu[batch] are left as they were (HYB_SLOT_NONE in one that this
         call makes)."""
         import torch
-        if cu is None:
-            cu = torch.empty(self.batch + 1, dtype=torch.int32, device=self.device)
-        if slots is None:
-            slots = torch.full((int(max_total),), _lib.HYB_SLOT_NONE, dtype=torch.int64, device=self.device)
+        total = int(max_total)
         for name, x in (("lens", lens), ("n_tok", n_tok), ("first", first)):
             if x is not None or name != "first":
                 self._check(x, (self.batch,), "BlockPool.slot_map: " + name)
-        self._check(cu, (self.batch + 1,), "BlockPool.slot_map: cu")
-        self._check(slots, (int(max_total),), "BlockPool.slot_map: slots", torch.int64)
-        _lib.on_device(self.device, stream, lambda s: _lib.hyb_slot_map(
-            self.desc, lens, first, n_tok, max_total, cu, slots, s))
-        return cu, slots
+        if cu is not None:
+            self._check(cu, (self.batch + 1,), "BlockPool.slot_map: cu")
+        if slots is not None:
+            self._check(slots, (total,), "BlockPool.slot_map: slots", torch.int64)
+        made = []
+
+        def call(s):
+            c, o = cu, slots
+            if c is None:
+                c = torch.empty(self.batch + 1, dtype=torch.int32, device=self.device)
+                made.append(c)
+            if o is None:
+                o = torch.full((total,), _lib.HYB_SLOT_NONE, dtype=torch.int64, device=self.device)
+                made.append(o)
+            _lib.hyb_slot_map(self.desc, lens, first, n_tok, total, c, o, s)
+            return c, o
+        return _lib.on_device(self.device, stream, call, made if cu is None or slots is None else None)
 
     def status(self, clear=False, stream=None):
         """The sticky device status word (0 = ok); waits for the stream."""

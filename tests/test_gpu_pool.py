@@ -208,3 +208,70 @@ def test_verification_steps_together():
         assert np.array_equal(got.transpose(1, 0, 2), kk[:, :c])
         ring = cache.hot[b].cpu().numpy().astype(np.float64)
         assert np.array_equal(ring[:, (-2 - s[c:]) % 32, 0], kk[:, c:]) and ((-2 - s[c:]) // 32 == b).all()
+
+
+def busy(stream, scratch):
+    """Copies that keep a stream at work for some milliseconds."""
+    import torch
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            scratch[1].copy_(scratch[0])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_on_another_stream_make_their_own_buffers(raw):
+    """tree_decode, resize in place and slot_map on a side stream, without
+    buffers, first while the current stream is at work, then while the side stream
+    is and the current one takes and fills memory of the same sizes."""
+    import torch
+    batch, hq, hkv, nodes, width = 6, 8, 2, 5, 6
+    rng = np.random.default_rng(3)
+    half = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float16)).cuda()  # noqa: E731
+    pool, model = BlockPool(batch, 40, width), PoolModel(batch, 40, width, 32, 64)
+    cache = HybridKVCache(batch, hkv, hq, 40, width, block_table=pool.block_table)
+    lens = np.array([0, 20, 100, 300, 33, 400])
+    model.resize(lens.tolist())
+    pool.resize(dev(lens))
+    cache.append(dev(lens), half(batch, 400, hkv, 128), half(batch, 400, hkv, 128))
+    q, k, v = half(batch, nodes, hq, 128), half(batch, nodes, hkv, 128), half(batch, nodes, hkv, 128)
+    n_tree = dev([5, 0, 3, 5, 1, 2])
+    want = cache.tree_decode(q, k, v, None, 0.09, n_tree=n_tree)
+    room = int(lens.sum()) + 9
+    want_cu, want_slots = pool.slot_map(dev(lens), dev(lens), room)
+    scratch = torch.empty((2, 1 << 28), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    for turn in range(4):
+        lens = rng.integers(0, 32 + 64 * width, size=batch)
+        now, of = dev(lens), dev([0, 20, 100, 300, 33, 400])
+        torch.cuda.synchronize()
+        busy(torch.cuda.current_stream() if turn % 2 == 0 else side, scratch)
+        got = cache.tree_decode(q, k, v, None, 0.09, n_tree=n_tree, stream=s)
+        cu, slots = pool.slot_map(of, of, room, stream=s) if turn == 0 else (want_cu, want_slots)
+        pool.resize(now, stream=s)
+        if turn % 2:
+            for n in (cache.tree_workspace(nodes).numel(), pool.workspace().numel(), 2 * q.numel()):
+                for _ in range(3):
+                    torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        refused = model.resize(lens.tolist())
+        assert_pool(pool, model, turn)
+        assert pool.status(clear=True) == (_lib.HYB_STATUS_POOL if refused else 0)
+        assert torch.equal(cu, want_cu) and torch.equal(slots, want_slots)
+        if turn == 0:
+            assert torch.equal(got, want)
+        else:                                      # the table is another one now
+            assert bool((got[1] == 0).all()) and bool((got[2, 3:] == 0).all())
+    assert torch.cuda.current_stream().cuda_stream != side.cuda_stream
+
+
+def test_the_stream_of_another_device_is_refused(monkeypatch):
+    import torch
+    pool = BlockPool(1, 4, 2)
+    other = torch.cuda.Stream()
+    pool.device = torch.device("cuda", torch.cuda.current_device() + 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: other)
+    monkeypatch.setattr(pool, "_check", lambda *a: None)
+    with pytest.raises(_lib.HybError):
+        pool.resize(dev([1]), stream=other)

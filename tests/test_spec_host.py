@@ -170,3 +170,42 @@ def test_references():
     assert s.tolist() == [9 * 64 + 2, 9 * 64 + 3, -2 - 68 % 32, -2 - 69 % 32]
     r = random_masks(np.random.default_rng(0), 2, 5, "any")
     assert (r[:, 0] == 0).all()
+
+
+def test_buffers_that_a_call_makes_are_made_on_its_stream(monkeypatch):
+    """tree_decode, resize and slot_map make and fill their own buffers inside
+    on_device, which makes the call's stream the current one."""
+    import torch
+    pool = hk.BlockPool(2, 8, 4, device="cpu")
+    c = object.__new__(hk.HybridKVCache)
+    c.batch, c.hkv, c.hq, c.device, c.desc = 2, 2, 4, torch.device("cpu"), _desc(hkv=2, hq=4)
+    q, k = torch.zeros((2, 3, 4, 128), dtype=torch.float16), torch.zeros((2, 3, 2, 128), dtype=torch.float16)
+    lens = torch.zeros(2, dtype=torch.int32)
+    inside, handed = [], []
+
+    def on_device(device, stream, call, made=None):
+        assert made is not None, "the call makes buffers"
+        inside.append(stream)
+        r = call(stream)
+        inside.pop()
+        handed.append(len(made))
+        return r
+
+    def watched(make):
+        def f(*a, **kw):
+            assert inside, "a buffer made outside the call's stream"
+            return make(*a, **kw)
+        return f
+
+    monkeypatch.setattr(_lib, "on_device", on_device)
+    for name in ("hyb_tree_attn", "hyb_pool_resize", "hyb_slot_map"):
+        monkeypatch.setattr(_lib, name, lambda *a: None)
+    for name in ("zeros", "empty", "full", "zeros_like", "empty_like", "full_like"):
+        monkeypatch.setattr(torch, name, watched(getattr(torch, name)))
+    out = c.tree_decode(q, k, k, None, 0.1, stream=5)
+    assert out.shape == q.shape and not out.any()
+    assert c.tree_decode(q, k, k, None, 0.1, out=q, stream=5) is q
+    assert pool.resize(lens, stream=5) is pool
+    cu, slots = pool.slot_map(lens, lens, 7, stream=5)
+    assert cu.shape == (3,) and slots.tolist() == [-1] * 7
+    assert handed == [1, 0, 0, 2]                 # what the caller gets

@@ -74,6 +74,24 @@ class HybridKVCache:
         d.status = self.status_word.data_ptr()
         return d
 
+    def _attend(self, call, out, make_out, workspace, make_workspace, stream):
+        """call(workspace, out, stream) -> out; buffers not given are made on the stream."""
+        made = []
+
+        def run(s):
+            ws = make_workspace() if workspace is None else workspace
+            o = out
+            if o is None:
+                o = make_out()
+                made.append(o)
+            call(ws, o, s)
+            return o
+        return _lib.on_device(self.device, stream, run, made if out is None or workspace is None else None)
+
+    def _empty_out(self):
+        import torch
+        return torch.empty((self.batch, self.hq, HEAD_DIM), dtype=torch.float16, device=self.device)
+
     # ---- the three calls ----
     def append(self, n_new, k_new, v_new, stream=None):
         """n_new: int32 CUDA [batch]; k_new, v_new: FP16 CUDA [batch][max_new][Hkv][128]."""
@@ -85,12 +103,16 @@ class HybridKVCache:
         [batch], host or CUDA), re-quantizing the blocks in between in place
         (hyb_kv_migrate).  max_delta: bound on the move (default: the table width)."""
         import torch
-        if self.n_int4 is None:
-            self.n_int4 = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
-            self.desc = self._make_desc()
-        tgt = torch.as_tensor(target_n_int4, dtype=torch.int32).to(self.device).contiguous()
-        md = self.max_blocks if max_delta is None else int(max_delta)
-        _lib.hyb_kv_migrate(self.desc, tgt, md, stream)
+        made = []
+
+        def call(s):
+            if self.n_int4 is None:
+                self.n_int4 = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
+                made.append(self.n_int4)
+                self.desc = self._make_desc()
+            tgt = torch.as_tensor(target_n_int4, dtype=torch.int32).to(self.device).contiguous()
+            _lib.hyb_kv_migrate(self.desc, tgt, self.max_blocks if max_delta is None else int(max_delta), s)
+        _lib.on_device(self.device, stream, call, made)
 
     def plan(self, max_seq_len, split_tokens=0):
         return _lib.hyb_decode_plan(self.desc, max_seq_len, split_tokens)
@@ -107,15 +129,10 @@ class HybridKVCache:
     def decode(self, q, softmax_scale, max_seq_len, split_tokens=0, out=None, lse=None,
                workspace=None, stream=None):
         """q: FP16 CUDA [batch][Hq][128] -> out FP16 [batch][Hq][128] (and lse FP32 [batch][Hq])."""
-        import torch
         assert q.is_contiguous()
-        if out is None:
-            out = torch.empty((self.batch, self.hq, HEAD_DIM), dtype=torch.float16, device=self.device)
-        if workspace is None:
-            workspace = self.workspace(max_seq_len, split_tokens)
-        _lib.hyb_decode_attn(self.desc, q, softmax_scale, max_seq_len, split_tokens, workspace,
-                             out, lse, stream)
-        return out
+        return self._attend(lambda ws, o, s: _lib.hyb_decode_attn(self.desc, q, softmax_scale, max_seq_len,
+                                                                  split_tokens, ws, o, lse, s),
+                            out, self._empty_out, workspace, lambda: self.workspace(max_seq_len, split_tokens), stream)
 
     def sparse_workspace(self, max_seq_len, split_tokens=0):
         import torch
@@ -126,15 +143,11 @@ class HybridKVCache:
                       workspace=None, stream=None):
         """As decode, but each query head attends only the top_k of the tokens
         in its sequence's INT4 (L2) blocks (hyb_decode_attn_sparse)."""
-        import torch
         assert q.is_contiguous()
-        if out is None:
-            out = torch.empty((self.batch, self.hq, HEAD_DIM), dtype=torch.float16, device=self.device)
-        if workspace is None:
-            workspace = self.sparse_workspace(max_seq_len, split_tokens)
-        _lib.hyb_decode_attn_sparse(self.desc, q, softmax_scale, max_seq_len, split_tokens, top_k, workspace,
-                                    out, lse, stream)
-        return out
+        return self._attend(lambda ws, o, s: _lib.hyb_decode_attn_sparse(self.desc, q, softmax_scale, max_seq_len,
+                                                                         split_tokens, top_k, ws, o, lse, s),
+                            out, self._empty_out, workspace,
+                            lambda: self.sparse_workspace(max_seq_len, split_tokens), stream)
 
     def sparse_selection(self, workspace, max_seq_len, split_tokens=0):
         """The selected L2 positions the last decode_sparse call with this
@@ -154,15 +167,11 @@ class HybridKVCache:
              lse=None, workspace=None, stream=None):
         """Fused decode step: append n_new[b] in {0, 1} tokens (k_new, v_new FP16
         [batch][1][Hkv][128]) and attend q; max_seq_len bounds the new lengths."""
-        import torch
         assert q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()
-        if out is None:
-            out = torch.empty((self.batch, self.hq, HEAD_DIM), dtype=torch.float16, device=self.device)
-        if workspace is None:
-            workspace = self.step_workspace(max_seq_len, split_tokens)
-        _lib.hyb_decode_step(self.desc, n_new, k_new, v_new, q, softmax_scale, max_seq_len, split_tokens,
-                             workspace, out, lse, stream)
-        return out
+        return self._attend(lambda ws, o, s: _lib.hyb_decode_step(self.desc, n_new, k_new, v_new, q, softmax_scale,
+                                                                  max_seq_len, split_tokens, ws, o, lse, s),
+                            out, self._empty_out, workspace, lambda: self.step_workspace(max_seq_len, split_tokens),
+                            stream)
 
     def tree_workspace(self, max_tree):
         """Workspace of tree_decode for trees of up to max_tree nodes (any lengths)."""
@@ -195,16 +204,10 @@ class HybridKVCache:
             need(x is None or (x.shape == shape and x.dtype == dtype and x.device == dev and x.is_contiguous()),
                  "tree_decode: " + name)
         need(workspace is None or (workspace.device == dev and workspace.is_contiguous()), "tree_decode: workspace")
-        made = []
-
-        def call(s):
-            ws = self.tree_workspace(nodes) if workspace is None else workspace
-            if out is None:
-                made.append(torch.zeros(q_shape, dtype=torch.float16, device=dev))
-            o = made[0] if out is None else out
-            _lib.hyb_tree_attn(self.desc, q, k_tree, v_tree, tree_mask, n_tree, nodes, softmax_scale, ws, o, lse, s)
-            return o
-        return _lib.on_device(dev, stream, call, made if out is None or workspace is None else None)
+        return self._attend(lambda ws, o, s: _lib.hyb_tree_attn(self.desc, q, k_tree, v_tree, tree_mask, n_tree, nodes,
+                                                                softmax_scale, ws, o, lse, s),
+                            out, lambda: torch.zeros(q_shape, dtype=torch.float16, device=dev),
+                            workspace, lambda: self.tree_workspace(nodes), stream)
 
     def status(self, clear=False, stream=None):
         return _lib.hyb_read_status(self.desc, clear, stream)

@@ -187,3 +187,32 @@ def test_step_into_unallocated_block():
     w.lens = ora.lens()
     assert_decode_close(w, out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy(), ref, ref_lse,
                         pairs=[(1, hh) for hh in range(8)], what="sequence 1")
+
+
+def test_calls_on_another_stream_make_their_own_buffers():
+    """decode, step, decode_sparse and migrate on a side stream, without buffers,
+    while the current stream is at work: what they do on the current one."""
+    import torch
+    w = synth.custom_workload("side", [900, 40, 2100, 33], 8, 2, seed=6, schedule="one", n_int4=[4, 0, 9, 0])
+    q = torch.from_numpy(synth.query(w)).cuda()
+    k, v = (torch.randn((4, 1, 2, 128), device="cuda").half() for _ in range(2))
+    n_new, target = torch.ones(4, dtype=torch.int32, device="cuda"), torch.tensor([2, 0, 12, 0], device="cuda")
+    scratch = torch.empty((2, 1 << 28), dtype=torch.uint8, device="cuda")
+    side, sides = torch.cuda.Stream(), []
+    for stream in (None, side, side.cuda_stream):
+        cache, _ = make_pair(w)
+        replay(w, cache, _)
+        torch.cuda.synchronize()
+        for i in range(20):
+            scratch[i & 1].copy_(scratch[~i & 1])
+        out = [cache.decode(q, w.softmax_scale, 2101, stream=stream)]
+        out.append(cache.decode_sparse(q, w.softmax_scale, 2101, 16, stream=stream))
+        out.append(cache.step(n_new, k, v, q, w.softmax_scale, 2101, stream=stream))
+        cache.migrate(target, stream=stream)
+        out.append(cache.decode(q, w.softmax_scale, 2101, stream=stream))
+        torch.cuda.synchronize()
+        assert cache.status() == 0
+        sides.append(out + [cache.cold, cache.scales, cache.n_int4])
+    for other in sides[1:]:
+        for x, y in zip(sides[0], other):
+            assert torch.equal(x, y)

@@ -209,3 +209,42 @@ def test_buffers_that_a_call_makes_are_made_on_its_stream(monkeypatch):
     cu, slots = pool.slot_map(lens, lens, 7, stream=5)
     assert cu.shape == (3,) and slots.tolist() == [-1] * 7
     assert handed == [1, 0, 0, 2]                 # what the caller gets
+
+
+def test_buffers_of_the_decode_calls_are_made_on_their_stream(monkeypatch):
+    """The same of decode, decode_sparse, step and migrate."""
+    import torch
+    c = object.__new__(hk.HybridKVCache)
+    c.batch, c.hkv, c.hq, c.device, c.desc, c.max_blocks = 2, 2, 4, torch.device("cpu"), _desc(hkv=2, hq=4), 16
+    c.n_int4, c._make_desc = None, lambda: _desc(hkv=2, hq=4)
+    q, k = torch.zeros((2, 4, 128), dtype=torch.float16), torch.zeros((2, 1, 2, 128), dtype=torch.float16)
+    n_new, target = torch.ones(2, dtype=torch.int32), torch.ones(2, dtype=torch.int64)
+    inside, handed = [], []
+
+    def on_device(device, stream, call, made=None):
+        assert made is not None and stream == 5
+        inside.append(stream)
+        r = call(stream)
+        inside.pop()
+        handed.append(len(made))
+        return r
+
+    def watched(make):
+        def f(*a, **kw):
+            assert inside, "a buffer made outside the call's stream"
+            return make(*a, **kw)
+        return f
+
+    monkeypatch.setattr(_lib, "on_device", on_device)
+    for name in ("hyb_decode_attn", "hyb_decode_attn_sparse", "hyb_decode_step", "hyb_kv_migrate"):
+        monkeypatch.setattr(_lib, name, lambda *a: None)
+    for name in ("zeros", "empty", "full", "as_tensor"):
+        monkeypatch.setattr(torch, name, watched(getattr(torch, name)))
+    assert c.decode(q, 0.1, 64, stream=5).shape == q.shape
+    assert c.decode(q, 0.1, 64, out=q, stream=5) is q
+    assert c.decode_sparse(q, 0.1, 64, 4, stream=5).shape == q.shape
+    assert c.step(n_new, k, k, q, 0.1, 64, stream=5).shape == q.shape
+    c.migrate(target, stream=5)
+    assert c.n_int4 is not None
+    c.migrate(target, stream=5)
+    assert handed == [1, 0, 1, 1, 1, 0]

@@ -7,8 +7,9 @@
 // O += P V.  INT8 / INT4 codes are integers that FP16 holds exactly, so K and
 // V enter the products as codes: a tile's K scale multiplies its logits, its V
 // scale the weights, both in FP32.  The weights p s_v / r are rounded once to
-// FP16 (half a step, 2^-11 relative; the tensor core takes no FP32 operand),
-// r being one of the V scales met, so that the FP16 range serves weights, not
+// FP16 (the tensor core takes no FP32 operand): half a step, 2^-11 relative, or
+// 2^-25 where p s_v / r is below 2^-14.  r is the tile's largest V scale where it
+// was set last (0 while all are 0), so that the FP16 range serves weights, not
 // scales: O holds the sum in units of r.  m may lag behind the maximum by
 // kLagLog2 (weights up to 2^6) and r behind the scales by kLagScale, so that O
 // is rescaled when they grow by much only; a weight stays below 2^14.  Products
@@ -923,8 +924,8 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
   const int part_row = (MT == 2 ? stream * 128 : 0) + row_in;
   // the row's state in the segment
   uint64_t odd = 0;  // attended nodes whose V is not finite
-  float m = -INFINITY, l = 0.f, ref = 1.f;
-  float inv = 1.f, minus_m = 0.f;  // 1 / ref, -m (0 while m is -inf)
+  float m = -INFINITY, l = 0.f, ref = 0.f;
+  float inv = 0.f, minus_m = 0.f;  // 1 / ref (0 while ref is 0), -m (0 while m is -inf)
   int ends = 0;      // segments
 
   for (int j = 0; j < n; j++) {
@@ -964,8 +965,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
       // them
       auto follow = [&](float top) -> bool {
         if (__builtin_expect(__any_sync(0xffffffffu, first || top > m + kLagLog2 || v_max > kLagScale * ref), 0)) {
-          float ref_new = first ? 1.f : ref;
-          if (v_max > 0.f && (first || v_max > kLagScale * ref)) ref_new = v_max;
+          const float ref_new = first || v_max > kLagScale * ref ? v_max : ref;
           const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
           if (!first) {
             // (MT 2: the stream's last P V is done, as this tile's S came after it)
@@ -973,7 +973,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
             if (MT == 1) tc_fence_after();
             const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
             l *= f;
-            const float g = f * __fdividef(ref, ref_new);
+            const float g = ref > 0.f ? f * __fdividef(ref, ref_new) : 0.f;  // (O is 0 while ref is)
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
               uint32_t o[16];
@@ -986,7 +986,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
           }
           m = m_new;
           ref = ref_new;
-          inv = __fdividef(1.f, ref);
+          inv = ref > 0.f ? __fdividef(1.f, ref) : 0.f;
           minus_m = m == -INFINITY ? 0.f : -m;
         }
         return true;

@@ -378,3 +378,30 @@ def test_two_row_tiles_with_short_trees(bits, hot, block):
     got, lse = run(cache, q, k, v, mask, n_tree, w.softmax_scale)
     check(w, ora, got, lse, q, k, v, mask, n_tree, w.softmax_scale)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("bits,sizes", [
+    (8, [0.0, 0.0, 1e-4, 1e-4, 1e-4, 1e-4]), (4, [0.0, 0.0, 3e-5, 3e-5, 3e-5, 3e-5]),
+    (8, [1e-4, 1e-4, 0.0, 0.0, 300.0, 300.0]), (8, [0.0, 0.0, 0.0, 0.0, 0.0, 0.0])])
+@pytest.mark.parametrize("nodes", [7, 64])        # one and two tiles of 128 rows per CTA
+def test_values_of_zero_or_far_apart_within_a_run(bits, sizes, nodes):
+    """Enough units that a CTA's run holds several whole ones: their tiles (of two
+    blocks each, the ring and the nodes last) have V of size `sizes`, zero first."""
+    import torch
+    rng = np.random.default_rng([nodes, bits])
+    lens = rng.integers(32 + 64 * 5, 32 + 64 * 6, size=90)
+    w = synth.custom_workload("zeros", [int(n) for n in lens], 16, 4, seed=6, schedule="chunk", chunk=64)
+    cache, ora = make_pair(w, quant_bits=bits)
+    for si, n in enumerate(w.schedule):
+        k, v = synth.step_tokens(w, si, n)
+        v = (v.astype(np.float32) * sizes[min(si, 5)]).astype(np.float16)
+        ora.append(n, k, v)
+        cache.append(torch.from_numpy(n).cuda(), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda())
+    q, kt, vt = inputs(w, nodes, 3)
+    vt = (vt.astype(np.float32) * sizes[5]).astype(np.float16)
+    n_tree = np.full(w.batch, nodes, np.int32)
+    if nodes > 7:                                  # (trees of 3, but for one: the reference's time)
+        n_tree[1:] = 3
+    got, lse = run(cache, q, kt, vt, None, n_tree, w.softmax_scale)
+    check(w, ora, got, lse, q, kt, vt, None, n_tree, w.softmax_scale, seqs=[0, 1, 2, 3, 30, 47, 60, 88, 89])
+    assert cache.status() == 0

@@ -962,9 +962,11 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
         if (r.keys < 64) nodes &= (1ull << r.keys) - 1;
       }
       // m and r follow the maxima when they lag too far behind; O and l follow
-      // them
+      // them.  Rows without a query have no say, and where m and r stay the factors
+      // are exactly 1: a row's bits do not depend on its neighbours, nor on what
+      // shared memory held
       auto follow = [&](float top) -> bool {
-        if (__builtin_expect(__any_sync(0xffffffffu, first || top > m + kLagLog2 || v_max > kLagScale * ref), 0)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, first || (live && top > m + kLagLog2) || v_max > kLagScale * ref), 0)) {
           const float ref_new = first || v_max > kLagScale * ref ? v_max : ref;
           const float m_new = first || top > m + kLagLog2 ? fmaxf(m, top) : m;
           if (!first) {
@@ -973,7 +975,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem<MT> &sm
             if (MT == 1) tc_fence_after();
             const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
             l *= f;
-            const float g = ref > 0.f ? f * __fdividef(ref, ref_new) : 0.f;  // (O is 0 while ref is)
+            const float g = ref_new == ref ? f : f * __fdividef(ref, ref_new);  // (O is 0 while ref is)
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
               uint32_t o[16];

@@ -405,3 +405,48 @@ def test_values_of_zero_or_far_apart_within_a_run(bits, sizes, nodes):
     got, lse = run(cache, q, kt, vt, None, n_tree, w.softmax_scale)
     check(w, ora, got, lse, q, kt, vt, None, n_tree, w.softmax_scale, seqs=[0, 1, 2, 3, 30, 47, 60, 88, 89])
     assert cache.status() == 0
+
+
+def growing(bits, lens):
+    """A cache whose keys grow along the sequence, so that a query of positive
+    values raises its maximum with every tile."""
+    import torch
+    w = synth.custom_workload("rows", lens, 16, 4, seed=5, schedule="one")
+    cache, _ = make_pair(w, quant_bits=bits)
+    k, v = synth.step_tokens(w, 0, w.schedule[0])
+    k = (np.abs(k.astype(np.float32)) * np.linspace(0.05, 4.0, k.shape[1])[None, :, None, None]).astype(np.float16)
+    cache.append(*(torch.from_numpy(x).cuda() for x in (w.schedule[0], k, v)))
+    return w, cache
+
+
+@pytest.mark.parametrize("bits", [8, 0])
+@pytest.mark.parametrize("nodes", [8, 64])        # one and two tiles of 128 rows per CTA
+def test_a_row_does_not_depend_on_its_neighbours(bits, nodes):
+    """Nodes 1.. with other queries leave node 0's bits alone: their maxima grow
+    tile by tile, or not at all."""
+    w, cache = growing(bits, [700 + 3 * i for i in range(40)])
+    q, kt, vt = inputs(w, nodes, 3)
+    mask = np.zeros((w.batch, nodes), np.int64)
+    out = []
+    for others in (0.0, 3.0):
+        q[:, 1:] = np.abs(q[:, 1:]) * 0 + others
+        out.append(run(cache, q, kt, vt, mask, None, w.softmax_scale))
+    assert np.array_equal(out[0][0][:, 0], out[1][0][:, 0]) and np.array_equal(out[0][1][:, 0], out[1][1][:, 0])
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("bits", [8, 0])
+@pytest.mark.parametrize("nodes", [8, 64])
+def test_results_repeat_whatever_ran_before(bits, nodes):
+    """A call whose trees leave rows of the tiles empty, after calls that left
+    other queries in shared memory."""
+    w, cache = growing(bits, [700 + 3 * i for i in range(40)])
+    q, kt, vt = inputs(w, nodes, 3)
+    few = np.full(w.batch, 1, np.int32)
+    out = []
+    for before in (0.0, 3.0, -3.0):
+        run(cache, np.full_like(q, before), kt, vt, None, None, w.softmax_scale)
+        out.append(run(cache, q, kt, vt, None, few, w.softmax_scale))
+    for o in out[1:]:
+        assert np.array_equal(o[0], out[0][0]) and np.array_equal(o[1], out[0][1])
+    assert cache.status() == 0

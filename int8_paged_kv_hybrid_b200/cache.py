@@ -6,6 +6,7 @@ include/hyb_kv.h.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 from . import _lib
@@ -74,6 +75,11 @@ class HybridKVCache:
         d.status = self.status_word.data_ptr()
         return d
 
+    def _here(self):
+        """The cache's device as the current one: sizes and plans go by its SM count."""
+        import torch
+        return torch.cuda.device(self.device) if self.device.type == "cuda" else contextlib.nullcontext()
+
     def _attend(self, call, out, make_out, workspace, make_workspace, stream):
         """call(workspace, out, stream) -> out; buffers not given are made on the stream."""
         made = []
@@ -115,15 +121,18 @@ class HybridKVCache:
         _lib.on_device(self.device, stream, call, made)
 
     def plan(self, max_seq_len, split_tokens=0):
-        return _lib.hyb_decode_plan(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            return _lib.hyb_decode_plan(self.desc, max_seq_len, split_tokens)
 
     def launch_info(self, max_seq_len, split_tokens=0):
         """(kernel, CTAs, CTAs per SM) of the decode launch for these arguments."""
-        return _lib.hyb_decode_launch_info(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            return _lib.hyb_decode_launch_info(self.desc, max_seq_len, split_tokens)
 
     def workspace(self, max_seq_len, split_tokens=0):
         import torch
-        n = _lib.hyb_decode_workspace_bytes(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            n = _lib.hyb_decode_workspace_bytes(self.desc, max_seq_len, split_tokens)
         return None if n == 0 else torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def decode(self, q, softmax_scale, max_seq_len, split_tokens=0, out=None, lse=None,
@@ -136,7 +145,8 @@ class HybridKVCache:
 
     def sparse_workspace(self, max_seq_len, split_tokens=0):
         import torch
-        n = _lib.hyb_decode_sparse_workspace_bytes(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            n = _lib.hyb_decode_sparse_workspace_bytes(self.desc, max_seq_len, split_tokens)
         return torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
 
     def decode_sparse(self, q, softmax_scale, max_seq_len, top_k, split_tokens=0, out=None, lse=None,
@@ -154,13 +164,15 @@ class HybridKVCache:
         workspace left: int32 CUDA view [batch][Hq][stride] (row (b, h): the
         first min(top_k, L2 tokens of b) entries, ascending)."""
         import torch
-        off, stride = _lib.hyb_decode_sparse_selection(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            off, stride = _lib.hyb_decode_sparse_selection(self.desc, max_seq_len, split_tokens)
         n = self.batch * self.hq * stride * 4
         return workspace[off:off + n].view(torch.int32).view(self.batch, self.hq, stride)
 
     def step_workspace(self, max_seq_len, split_tokens=0):
         import torch
-        n = _lib.hyb_decode_step_workspace_bytes(self.desc, max_seq_len, split_tokens)
+        with self._here():
+            n = _lib.hyb_decode_step_workspace_bytes(self.desc, max_seq_len, split_tokens)
         return torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
 
     def step(self, n_new, k_new, v_new, q, softmax_scale, max_seq_len, split_tokens=0, out=None,
@@ -176,7 +188,8 @@ class HybridKVCache:
     def tree_workspace(self, max_tree):
         """Workspace of tree_decode for trees of up to max_tree nodes (any lengths)."""
         import torch
-        n = _lib.hyb_tree_workspace_bytes(self.desc, max_tree)
+        with self._here():
+            n = _lib.hyb_tree_workspace_bytes(self.desc, max_tree)
         _lib.need(n > 0, "tree_workspace: max_tree %r" % (max_tree,))
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 

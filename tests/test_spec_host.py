@@ -248,3 +248,37 @@ def test_buffers_of_the_decode_calls_are_made_on_their_stream(monkeypatch):
     assert c.n_int4 is not None
     c.migrate(target, stream=5)
     assert handed == [1, 0, 1, 1, 1, 0]
+
+
+def test_sizes_and_plans_are_asked_on_the_caches_device(monkeypatch):
+    """The current device is another one than the cache's."""
+    import contextlib
+
+    import torch
+    c = object.__new__(hk.HybridKVCache)
+    c.batch, c.hkv, c.hq, c.device, c.desc = 2, 2, 4, torch.device("cuda", 1), _desc(hkv=2, hq=4)
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d.index)
+        yield
+        current.pop()
+
+    def size(*a):
+        asked.append(current[-1])
+        return 64
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    names = ["hyb_tree_workspace_bytes", "hyb_decode_workspace_bytes", "hyb_decode_step_workspace_bytes",
+             "hyb_decode_sparse_workspace_bytes", "hyb_decode_plan", "hyb_decode_launch_info"]
+    for name in names:
+        monkeypatch.setattr(_lib, name, size)
+    monkeypatch.setattr(_lib, "hyb_decode_sparse_selection", lambda *a: (0, size()))
+    for make in ("empty", "zeros"):
+        monkeypatch.setattr(torch, make, lambda n, **kw: kw["device"].index)
+    assert c.tree_workspace(4) == 1 and c.workspace(99) == 1 and c.step_workspace(99) == 1 and c.sparse_workspace(99) == 1
+    c.plan(99)
+    c.launch_info(99)
+    c.sparse_selection(torch.arange(4096, dtype=torch.uint8), 99)
+    assert asked == [1] * 7 and current == [0]

@@ -102,7 +102,8 @@ class HybridKVCache:
     def append(self, n_new, k_new, v_new, stream=None):
         """n_new: int32 CUDA [batch]; k_new, v_new: FP16 CUDA [batch][max_new][Hkv][128]."""
         assert k_new.is_contiguous() and v_new.is_contiguous() and n_new.is_contiguous()
-        _lib.hyb_kv_append(self.desc, n_new, k_new.shape[1], k_new, v_new, stream)
+        _lib.on_device(self.device, stream, lambda s: _lib.hyb_kv_append(self.desc, n_new, k_new.shape[1], k_new,
+                                                                         v_new, s))
 
     def migrate(self, target_n_int4, max_delta=None, stream=None):
         """Move every sequence's INT4 block count to target_n_int4 (int32
@@ -223,7 +224,7 @@ class HybridKVCache:
                             workspace, lambda: self.tree_workspace(nodes), stream)
 
     def status(self, clear=False, stream=None):
-        return _lib.hyb_read_status(self.desc, clear, stream)
+        return _lib.on_device(self.device, stream, lambda s: _lib.hyb_read_status(self.desc, clear, s))
 
 
 def default_softmax_scale(head_dim=HEAD_DIM):

@@ -282,3 +282,17 @@ def test_sizes_and_plans_are_asked_on_the_caches_device(monkeypatch):
     c.launch_info(99)
     c.sparse_selection(torch.arange(4096, dtype=torch.uint8), 99)
     assert asked == [1] * 7 and current == [0]
+
+
+def test_append_and_status_go_to_the_caches_device(monkeypatch):
+    """As the other calls: the stream is one of the cache's device, not of the current one."""
+    import torch
+    c = object.__new__(hk.HybridKVCache)
+    c.device, c.desc = torch.device("cuda", 1), _desc()
+    went = []
+    monkeypatch.setattr(_lib, "on_device", lambda device, stream, call, made=None: (went.append(device), call(stream))[1])
+    monkeypatch.setattr(_lib, "hyb_kv_append", lambda *a: went.append(a[-1]))
+    monkeypatch.setattr(_lib, "hyb_read_status", lambda *a: 9)
+    x = torch.zeros((1, 2, 3))
+    c.append(x, x, x, stream=5)
+    assert c.status(stream=6) == 9 and went == [c.device, 5, c.device]

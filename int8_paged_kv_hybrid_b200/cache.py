@@ -75,6 +75,17 @@ class HybridKVCache:
         d.status = self.status_word.data_ptr()
         return d
 
+    def use_table(self, block_table):
+        """Go on with another block table, from the next call on: int32
+        [batch][max_blocks_per_seq], contiguous, on the cache's device; it is kept,
+        not copied.  This is how the table of a pool's successor gets here.  A
+        captured call stays with the table that it was captured with."""
+        import torch
+        _lib.need(block_table.shape == self.block_table.shape and block_table.dtype == torch.int32 and
+                  block_table.device == self.device and block_table.is_contiguous(), "use_table")
+        self.block_table = block_table
+        self.desc.block_table = block_table.data_ptr()
+
     def _here(self):
         """The cache's device as the current one: sizes and plans go by its SM count."""
         import torch

@@ -34,7 +34,8 @@ class BlockPool:
     by the sequences of a batch (hyb_pool_desc).  A new pool has every block
     free.  Existing buffers may be given: ring int32 [num_phys_blocks], state
     int32 [2] (head, count), n_blocks int32 [batch], block_table int32
-    [batch][max_blocks_per_seq].  `block_table` is what HybridKVCache takes.
+    [batch][max_blocks_per_seq].  `block_table` is what HybridKVCache takes
+    (a successor's: HybridKVCache.use_table).
     A call works on `stream` (default: the current one of the pool's device),
     where the buffers that it is not given are made too."""
 

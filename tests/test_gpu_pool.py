@@ -275,3 +275,34 @@ def test_the_stream_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(pool, "_check", lambda *a: None)
     with pytest.raises(_lib.HybError):
         pool.resize(dev([1]), stream=other)
+
+
+def test_steps_with_successors():
+    """Each step's tables are built into the other of two pools, which the cache
+    then takes: appends and attention as with one table resized in place."""
+    import torch
+    batch, hq, hkv, nodes, width = 4, 8, 2, 4, 8
+    rng = np.random.default_rng(5)
+    half = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float16)).cuda()  # noqa: E731
+    pools = [BlockPool(batch, 30, width)]
+    pools.append(pools[0].successor())
+    inplace = BlockPool(batch, 30, width)
+    cache, other = (HybridKVCache(batch, hkv, hq, 30, width, block_table=p.block_table) for p in (pools[0], inplace))
+    lens = np.zeros(batch, int)
+    for step in range(5):
+        n = rng.integers(0, 90, size=batch)
+        lens = lens + n
+        now = pools[step % 2].resize(dev(lens + nodes), to=pools[1 - step % 2])
+        cache.use_table(now.block_table)
+        inplace.resize(dev(lens + nodes))
+        assert torch.equal(now.block_table, inplace.block_table)
+        k, v = half(batch, 90, hkv, 128), half(batch, 90, hkv, 128)
+        q, kt, vt = half(batch, nodes, hq, 128), half(batch, nodes, hkv, 128), half(batch, nodes, hkv, 128)
+        outs = []
+        for c in (cache, other):
+            c.append(dev(n), k, v)
+            outs.append(c.tree_decode(q, kt, vt, None, 0.09))
+            assert c.status() == 0
+        assert torch.equal(outs[0], outs[1]) and torch.equal(cache.cold, other.cold)
+        pools[step % 2].block_table.fill_(-7)       # the table of the last step is not read any more
+    assert pools[0].status() == 0 and inplace.status() == 0

@@ -296,3 +296,16 @@ def test_append_and_status_go_to_the_caches_device(monkeypatch):
     x = torch.zeros((1, 2, 3))
     c.append(x, x, x, stream=5)
     assert c.status(stream=6) == 9 and went == [c.device, 5, c.device]
+
+
+def test_use_table():
+    import torch
+    c = object.__new__(hk.HybridKVCache)
+    c.device, c.desc, c.block_table = torch.device("cpu"), _desc(), torch.zeros((2, 4), dtype=torch.int32)
+    t = torch.ones((2, 4), dtype=torch.int32)
+    for bad in (t[:1], t.long(), torch.ones((4, 2), dtype=torch.int32).t(), torch.ones((2, 5), dtype=torch.int32)[:, :4]):
+        with pytest.raises(hk.HybError):
+            c.use_table(bad)
+    desc = c.desc
+    c.use_table(t)
+    assert c.block_table is t and c.desc is desc and desc.block_table == t.data_ptr()

@@ -209,13 +209,12 @@ class HybridKVCache:
                     workspace=None, stream=None):
         """Attention of drafted nodes (hyb_tree_attn) on `stream` (default: the
         current one of the cache's device), where buffers not given are made too:
-        q FP16 CUDA
-        [batch][nodes][Hq][128], k_tree / v_tree FP16 [batch][nodes][Hkv][128],
-        tree_mask int64 [batch][nodes] (bit j: the node attends node j; see
-        tree_masks) or None for a chain, n_tree int32 [batch] or None for all
-        nodes -> out FP16 [batch][nodes][Hq][128] (and lse FP32
-        [batch][nodes][Hq]).  Rows at and behind n_tree[b] are left as they
-        were (zero, and -inf, in an `out` and a `lse` that this call makes)."""
+        q FP16 CUDA [batch][nodes][Hq][128], k_tree / v_tree FP16
+        [batch][nodes][Hkv][128], tree_mask int64 [batch][nodes] (bit j: the node
+        attends node j; see tree_masks) or None for a chain, n_tree int32 [batch] or
+        None for all nodes -> out FP16 [batch][nodes][Hq][128], and into `lse` FP32
+        [batch][nodes][Hq] where it is given.  Rows at and behind n_tree[b] are left
+        as they were (zero in an `out` that this call makes)."""
         import torch
         need, dev, nodes = _lib.need, self.device, q.shape[1] if q.dim() == 4 else 0
         q_shape, kv_shape = (self.batch, nodes, self.hq, HEAD_DIM), (self.batch, nodes, self.hkv, HEAD_DIM)

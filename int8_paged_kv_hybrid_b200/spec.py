@@ -15,11 +15,11 @@ def tree_masks(parents):
     """Ancestor masks of a drafted tree: parents[t] < t is the parent node of
     node t, or -1 for a child of the last cached token.  Returns int64 masks of
     the same shape (bit j of mask t: node t is j or descends from it); the last
-    axis is the nodes, at most 64.  Host only."""
-    p = np.asarray(parents, np.int64)
-    nodes = p.shape[-1]
-    if nodes > _lib.HYB_MAX_TREE or ((p < -1) | (p >= np.arange(nodes))).any():
-        raise _lib.HybError(_lib.HYB_ERR_INVALID_VALUE, "tree_masks")
+    axis is the nodes, 1 to 64.  Host only."""
+    p = np.asarray(parents)
+    _lib.need(p.dtype.kind in "iu" and p.ndim > 0 and 1 <= p.shape[-1] <= _lib.HYB_MAX_TREE, "tree_masks")
+    p, nodes = p.astype(np.int64), p.shape[-1]
+    _lib.need(((p >= -1) & (p < np.arange(nodes))).all(), "tree_masks")
     flat = p.reshape(-1, nodes)
     mask = np.zeros(flat.shape, np.uint64)
     rows = np.arange(flat.shape[0])

@@ -309,3 +309,16 @@ def test_use_table():
     desc = c.desc
     c.use_table(t)
     assert c.block_table is t and c.desc is desc and desc.block_table == t.data_ptr()
+
+
+@pytest.mark.parametrize("bad", [[], [[], []], 0, -1, [-1.0, 0.4], [True], ["a"], [None], [-1, 2 ** 70]])
+def test_tree_masks_refuses_what_is_no_tree(bad):
+    """No nodes, no axis of nodes, and parents that are no whole numbers."""
+    with pytest.raises(hk.HybError):
+        hk.tree_masks(bad)
+
+
+def test_tree_masks_of_whole_numbers_of_any_type():
+    for t in (np.int8, np.int32, np.int64):
+        assert hk.tree_masks(np.array([-1, 0, 0], t)).tolist() == [1, 3, 5]
+    assert hk.tree_masks(np.zeros((0, 3), np.int32)).shape == (0, 3)

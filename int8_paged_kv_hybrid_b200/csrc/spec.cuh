@@ -66,13 +66,8 @@ struct SlotArgs {
 };
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t stream);
-// 128-row tiles a CTA takes at once for trees of max_tree nodes, and the row
-// groups of that many tiles a (sequence, kv head) can have
+// 128-row tiles a CTA takes at once for trees of max_tree nodes
 inline int tree_m_tiles(int max_tree, int group) { return max_tree * group > 128 ? 2 : 1; }
-inline int tree_groups(int max_tree, int group) {
-  const int rows = 128 * tree_m_tiles(max_tree, group);
-  return (max_tree * group + rows - 1) / rows;
-}
 cudaError_t launch_pool_resize(const PoolArgs &a, int sms, cudaStream_t stream);
 cudaError_t launch_slot_map(const SlotArgs &a, int sms, cudaStream_t stream);
 

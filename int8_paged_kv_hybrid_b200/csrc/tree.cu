@@ -83,9 +83,8 @@ constexpr int kTreeSoftRegs = 120, kTreeProdRegs = 72;
 // that this CTA has); every key attended by every row and no
 // negative scale; cold (not ring and nodes); the segment has the unit's first,
 // its last tile; the segment's number modulo 4
-constexpr uint32_t kTileFirst = 1, kTileLast = 4, kTilePlain = 8, kTileCold = 16, kUnitStart = 32,
-                   kUnitEnd = 64;
-constexpr int kTileSegShift = 7;
+constexpr uint32_t kTileFirst = 1, kTileLast = 2, kTilePlain = 4, kTileCold = 8, kUnitStart = 16, kUnitEnd = 32;
+constexpr int kTileSegShift = 6;
 
 // A tile of 128 keys in four units of 32, as the scout found it.
 struct TreeRec {
@@ -179,17 +178,16 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
 }
 
 // Wait for phase `parity`; false when the wait or the kernel gave up.  By a whole
-// warp, with one answer, or (kOne) by one thread.  Small, as it stands at many places.
-template <bool kOne = false, typename Sm>
+// warp, with one answer.  Small, as it stands at many places.
+template <typename Sm>
 __device__ __forceinline__ bool tree_wait(Sm &sm, uint64_t *bar, uint32_t parity, const TreeArgs &a) {
   uint32_t t0 = 0;
 #pragma unroll 1
   for (;;) {
-    const bool ok = mbar_try_wait(bar, parity);
-    if (kOne ? ok : __all_sync(0xffffffffu, ok)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint32_t t = static_cast<uint32_t>(clock()) | 1;
     if (t0 == 0) t0 = t;
-    if (kOne ? sm.abort || t - t0 > a.wait_cycles : __any_sync(0xffffffffu, sm.abort || t - t0 > a.wait_cycles)) break;
+    if (__any_sync(0xffffffffu, sm.abort || t - t0 > a.wait_cycles)) break;
   }
   sm.abort = 1;
   return false;

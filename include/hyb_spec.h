@@ -65,7 +65,8 @@ extern "C" {
  *            contents need no preparation.  Calls that share it must not
  *            overlap on the GPU.
  *   out      device FP16 [batch][max_tree][Hq][D] (round to nearest even),
- *            16-byte aligned.  Rows t >= n_tree[b] are left as they were.
+ *            16-byte aligned.  Rows t >= n_tree[b] are left as they were.  It may
+ *            be q itself; otherwise out and lse_out overlap no input.
  *   lse_out  device FP32 [batch][max_tree][Hq], natural log, or NULL; likewise.
  * The cache is only read.  Nothing is sized by the lengths: a captured call
  * may be replayed after the sequences grew.

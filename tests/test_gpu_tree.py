@@ -450,3 +450,44 @@ def test_results_repeat_whatever_ran_before(bits, nodes):
     for o in out[1:]:
         assert np.array_equal(o[0], out[0][0]) and np.array_equal(o[1], out[0][1])
     assert cache.status() == 0
+
+
+def test_a_single_node_over_fp16_cold_blocks_is_a_decode_step():
+    """FP16 cold blocks hold the tokens as they came: a cache of L tokens that is
+    decoded, and one of L - 1 tokens under a tree of the last one, attend the same
+    values.  The decode call has its accuracy bar, the tree its bound."""
+    import torch
+    from harness import MAX_ABS
+    w = synth.custom_workload("last", [33, 65, 90, 129, 500, 1201], 8, 2, seed=4, schedule="one")
+    k, v = synth.step_tokens(w, 0, w.schedule[0])
+    n = w.schedule[0]
+    whole, _ = make_pair(w, quant_bits=0)
+    whole.append(*(torch.from_numpy(x).cuda() for x in (n, k, v)))
+    cache, ora = make_pair(w, quant_bits=0)
+    cache.append(*(torch.from_numpy(x).cuda() for x in (n - 1, k, v)))
+    ora.append(n - 1, k, v)
+    q, _, _ = inputs(w, 1, 1)
+    last = np.arange(w.batch), n - 1
+    kt, vt = np.ascontiguousarray(k[last][:, None]), np.ascontiguousarray(v[last][:, None])
+    got, lse = run(cache, q, kt, vt, None, None, w.softmax_scale)
+    check(w, ora, got, lse, q, kt, vt, None, None, w.softmax_scale)
+    step = whole.decode(torch.from_numpy(q[:, 0]).cuda(), w.softmax_scale, int(n.max())).float().cpu().numpy()
+    for b in range(w.batch):
+        kk, vv = cached_kv(ora, b, int(n[b]) - 1)
+        _, _, tol, _ = tree_attention(kk, vv, q[b], kt[b], vt[b], np.ones(1, np.int64), 1, w.softmax_scale)
+        assert (np.abs(got[b, 0] - step[b]) <= tol[0] + MAX_ABS).all(), b
+
+
+@pytest.mark.parametrize("nodes", [5, 64])
+def test_the_output_may_be_the_queries(nodes):
+    """In place: whole units, shared ones and values that are not finite."""
+    import torch
+    w = synth.custom_workload("place", [0, 40, 700, 3000], 16, 4, seed=4)
+    cache, ora = make_pair(w)
+    replay(w, cache, ora)
+    q, k, v = inputs(w, nodes, 2)
+    v[1, 1, 0, 7] = np.inf
+    q, k, v = (torch.from_numpy(x).cuda() for x in (q, k, v))
+    want = cache.tree_decode(q, k, v, None, w.softmax_scale)
+    assert cache.tree_decode(q, k, v, None, w.softmax_scale, out=q) is q
+    assert torch.equal(q, want) and bool(torch.isinf(want).any())

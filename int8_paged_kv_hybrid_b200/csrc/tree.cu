@@ -36,17 +36,27 @@
 // two buffers, so that Q K^T of the next tile (one MMA warp) runs behind it and
 // P V of the last one (the other).
 //
-// What bounds it (measured with the L2 flushed, us; "long": 4 sequences of 32768
-// .. 131072 tokens, 32 nodes, 32 heads, 8 kv heads; "short trees": 64 sequences of
-// 256 .. 8192 tokens, 8 nodes; "wide": 8 of 16384 tokens, 64 nodes, 64 heads).  No
-// unit is busy most of the time: of long's 241 us the bytes need 101 and the
-// products 103.  The time goes to instructions: six roles on one SM, whose code
-// has to come from its instruction cache (with 110 KB of unrolled code 31% of the
-// requests missed and a stall for instructions was the commonest: long 372; as
-// loops, 86 KB: 285), and to the softmax warps' path from one tile to the next,
-// about 2500 cycles, of which two warps' powers of two take 1120 and the waits,
-// records, the TMEM round trip and the arrival 1400 whatever the rows and keys
-// are.  What was tried:
+// What bounds it (us with the L2 flushed before each call; "long": 4 sequences of
+// 32768 .. 131072 tokens, 32 nodes, 32 heads, 8 kv heads: 242; "short trees": 64
+// sequences of 256 .. 8192 tokens, 8 nodes: 314; "wide": 8 of 16384 tokens, 64
+// nodes, 64 heads: 383).  No unit is busy most of the time: of long's 242 us the
+// bytes need 101 and the products 103.  In SM cycles, by a clock read per tile (the
+// SMs run at about 1840 MHz inside a call, at 1600 .. 1750 when long calls follow
+// each other under the power limit):
+//   a cold tile: 2450 (32 query rows) .. 2640 (128), with INT4 among them 2760, of
+//   FP16 rows 4000, MT 2 5550.  The first is the softmax warps' path from one tile
+//   to the next: two warps' powers of two take 1120, and the waits, records, the
+//   TMEM round trip and the arrival about 1400 whatever the rows and keys are
+//   the end of a unit: its tail tile 11000 .. 13500 (the ring and the nodes are
+//   loaded when its turn has come), the next unit's first tile 5700 .. 6600
+//   a call's begin: 4500 until the roles start, 15000 until the first weights
+//   (18500 with the L2 flushed); the merge: 1 us behind the last CTA, 5 .. 9 us long
+// Runs are cut by tiles, not by time: short trees' runs have 2 .. 16 ends of units,
+// and half of the CTAs are done after 196 of the 297 us that the last one takes
+// (long: 208 of 223).  Instruction supply bounded it before, as six roles share an
+// SM's instruction cache: with 110 KB of unrolled code 31% of the requests missed and
+// a stall for instructions was the commonest (long 372; as loops, 86 KB: 285).  What
+// was tried:
 //   a lane per ring piece issues the copies, instead of one thread: long 283 -> 261
 //   64 logits stay in registers between maximum and weights (MT 1): long 262 -> 247
 //   K and V producers share their code: short trees 354 -> 342
